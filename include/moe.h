@@ -410,6 +410,113 @@ MOE_API int moe_decode_layer(const moe_forward_args* a, const float* router_logi
                              int32_t* topk_ids_out, float* topk_weights_out, uint32_t* sync, void* workspace,
                              int64_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the layer: what feeds it, and an expert's MLP in pieces
+ * for the experts that moe_forward does not run (a shared expert every token
+ * passes, experts whose rows an expert-parallel exchange delivered already
+ * sorted).  Quantised rows are in moe_quant_act's format (E4M3FN codes, fp32
+ * power-of-two scales per row and 128 columns) or moe_quant_act_mx's (E8M0
+ * bytes per 32 columns); `quant` names it: MOE_WDTYPE_FP8_E4M3 or
+ * MOE_WDTYPE_MXFP8, MOE_WDTYPE_BF16 for no codes.
+ * ------------------------------------------------------------------------ */
+#define MOE_MAX_NORM_COLS 32768
+
+/*
+ * moe_rmsnorm — residual addition and RMSNorm in front of the layer, with its
+ * fp8 quantisation (P2 section 1.2's scale rule, moe_quant_act's) where the
+ * next products take codes.  Per row:
+ *   s = fl32(x + residual)                 (s = x without a residual)
+ *   residual_out = bf16(s)
+ *   y = bf16(s * weight / sqrt(mean(s^2) + eps))
+ *   codes, scales = moe_quant_act(y) or moe_quant_act_mx(y)
+ * The mean and the products behind y are held in fp64 and rounded once to
+ * fp32 and then bf16, so codes and scales do not depend on the launch shape.
+ *
+ *   x             device, bf16 [rows, cols]
+ *   residual      device, bf16 [rows, cols] or NULL
+ *   weight        device, bf16 [cols]
+ *   residual_out  device, bf16 [rows, cols] or NULL  (output; needs residual)
+ *   y             device, bf16 [rows, cols] or NULL  (output)
+ *   codes         device, E4M3FN [rows, cols]; NULL for MOE_WDTYPE_BF16 (output)
+ *   scales        device, fp32 [rows, cols / 128] or E8M0 [rows, cols / 32]
+ *                 (4-byte aligned); NULL for MOE_WDTYPE_BF16 (output)
+ * residual_out and y may each be x or residual itself (not each other); no
+ * output may overlap an input or another output otherwise.  At least one
+ * output is required.  eps >= 0 and finite (a row of zeros with eps 0 is NaN);
+ * a NaN or an infinity in a row makes that row's results unspecified.
+ * Requires cols % 8 == 0 (FP8_E4M3: % 128, MXFP8: % 32) and cols <=
+ * MOE_MAX_NORM_COLS, else MOE_ERR_UNSUPPORTED.
+ */
+MOE_API int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int32_t rows,
+                        int32_t cols, int32_t quant, void* residual_out, void* y, uint8_t* codes, void* scales,
+                        hipStream_t stream);
+
+/*
+ * moe_silu_mul — the SiLU-gated multiply between an expert's two products,
+ * with its quantisation (the fused kernel of P2 section 1.2 as an operator of
+ * its own).  Per row of gate g = h[0 .. cols) and up u = h[cols .. 2 cols):
+ *   clamp_limit L > 0:  g = min(g, L), u = min(max(u, -L), L)
+ *   y = bf16(bf16(silu(g)) * u), silu(g) = g / (1 + exp(-g))
+ *   codes, scales = moe_quant_act(y) or moe_quant_act_mx(y)
+ * bf16(silu(g)) is the correctly rounded value for every finite g.
+ *
+ *   h       device, bf16 [rows, 2 * cols] (a w13 product's rows)
+ *   y       device, bf16 [rows, cols]; NULL allowed when quant makes codes (output)
+ *   codes, scales  as for moe_rmsnorm (output)
+ * No output may overlap h or another output.  clamp_limit >= 0 (0: none).  A
+ * NaN or an infinity makes its quantisation group's results unspecified.
+ * Requires cols % 8 == 0 (FP8_E4M3: % 128, MXFP8: % 32) and cols <= 2^20.
+ */
+MOE_API int moe_silu_mul(const void* h, int32_t rows, int32_t cols, float clamp_limit, int32_t quant, void* y,
+                         uint8_t* codes, void* scales, hipStream_t stream);
+
+/*
+ * moe_gemm_fp8 — dense product of quantised rows with block-scaled weights
+ * (the block-fp8 scheme of P2 section 1.1 without experts):
+ *   out[m, n] = bf16(sum_b a_scale[m, b] w_scale[n / 128, b] p(m, n, b)),
+ *   p(m, n, b) = sum of a[m, k] w[n, k] over the 128 k of block b.
+ * p runs on the fp8 matrix cores, whose dot product drops terms below about
+ * 2^-14 of the largest in its group (~1e-4 of a block's sum of magnitudes, a
+ * fraction of the output's bf16 rounding); everything else is fp32.
+ *
+ *   a        device, E4M3FN [M, K]
+ *   a_scale  device, fp32 [M, K / 128] (any finite values)
+ *   w        device, E4M3FN [N, K]
+ *   w_scale  device, fp32 [ceil(N / 128), K / 128]
+ *   out      device, bf16 [M, N]   (output; must not overlap an input)
+ *   workspace  device, >= moe_gemm_fp8_workspace(M, N, K) bytes, 256-byte
+ *              aligned; NULL when that is 0; contents on entry do not matter
+ * Requires N >= 1, K % 128 == 0, 128 <= K <= 2^20 and M, N <= 2^30.
+ */
+MOE_API int64_t moe_gemm_fp8_workspace(int32_t M, int32_t N, int32_t K);
+MOE_API int moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int32_t M,
+                         int32_t N, int32_t K, void* out, void* workspace, int64_t workspace_bytes,
+                         hipStream_t stream);
+
+/*
+ * moe_grouped_gemm — products of rows that are already sorted by expert, the
+ * groups ragged and unpadded (the sorted rows of P2 section 1.1 without the
+ * block padding):
+ *   out[r, n] = bf16(sum_k a[r, k] w[e, n, k]) for offsets[e] <= r < offsets[e+1]
+ * in bf16 (fp32 sums), or in fp8 with moe_gemm_fp8's scales and arithmetic.
+ * Rows outside every group (before offsets[0], from offsets[E] on) are neither
+ * read nor written; groups may be empty.
+ *
+ *   a        device, bf16 or E4M3FN [rows, K]
+ *   a_scale  device, fp32 [rows, K / 128] (FP8_E4M3), else NULL
+ *   w        device, bf16 or E4M3FN [E, N, K]
+ *   w_scale  device, fp32 [E, ceil(N / 128), K / 128] (FP8_E4M3), else NULL
+ *   offsets  device, int32 [E + 1], ascending, in [0, rows] (a table that is
+ *            not gives unspecified rows, never an access out of bounds)
+ *   out      device, bf16 [rows, N]   (output; must not overlap an input)
+ * wdtype is MOE_WDTYPE_BF16 or MOE_WDTYPE_FP8_E4M3 (MXFP8: MOE_ERR_UNSUPPORTED).
+ * Requires 1 <= E <= MOE_MAX_EXPERTS, N >= 1, K % 64 == 0 (bf16) or K % 128
+ * == 0 (fp8), K <= 2^20, and rows, N <= 2^30.
+ */
+MOE_API int moe_grouped_gemm(const void* a, const float* a_scale, const void* w, const float* w_scale,
+                             const int32_t* offsets, int32_t rows, int32_t E, int32_t N, int32_t K, int32_t wdtype,
+                             void* out, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,125 @@
+// Residual add + RMSNorm (+ fp8 quantisation) of bf16 rows:
+//   s = fl32(x + r);  r' = bf16(s);  y = bf16(s * w / sqrt(mean(s^2) + eps));
+//   codes and scales of y by moe_quant_act's rule.
+//
+// The mean of squares and the two products behind y are computed in fp64 and
+// rounded to fp32 and then bf16 once, so y (and with it the codes and scales,
+// whose scale doubles at a border of the group's maximum) does not depend on
+// the order of the sum: the result is the same for every launch shape.
+//
+// One workgroup per row, the row held in registers between the two passes, so
+// it is read once and every load of a row precedes its first store (the
+// outputs may replace the inputs).  A thread holds CH chunks of 8 columns
+// (16 bytes); a 128-column quantisation group is 16 neighbouring lanes.
+// HBM-bound: 2 bytes read (4 with a residual), 2 written for each of r' and y,
+// 1 + 4/128 for the codes and scales.
+#include "dense.h"
+
+namespace moe {
+
+namespace {
+
+template <int NT, int CH, int kQuant>
+__global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
+    __shared__ double s_part[NT / 64];
+    const int64_t row = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+    if (row >= a.rows) return;
+    const int nvec = a.cols >> 3;
+    const uint16_t* x = a.x + row * a.cols;
+    const uint16_t* r = a.residual ? a.residual + row * a.cols : nullptr;
+
+    float v[CH][8];
+    i32x4 w[CH];
+    double sum = 0.0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = threadIdx.x + c * NT;
+        // without a residual r = -0, which leaves every x as it is
+        constexpr int kNegZero = int(0x80008000u);
+        i32x4 xv = {0, 0, 0, 0}, rv = {kNegZero, kNegZero, kNegZero, kNegZero};
+        w[c] = i32x4{0, 0, 0, 0};
+        if (i < nvec) {
+            xv = *reinterpret_cast<const i32x4*>(x + i * 8);
+            if (r) rv = *reinterpret_cast<const i32x4*>(r + i * 8);
+            w[c] = *reinterpret_cast<const i32x4*>(a.weight + i * 8);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[c][2 * q] = __fadd_rn(bf16_lo(xv[q]), bf16_lo(rv[q]));
+            v[c][2 * q + 1] = __fadd_rn(bf16_hi(xv[q]), bf16_hi(rv[q]));
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum = __fma_rn(double(v[c][q]), double(v[c][q]), sum);
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) sum += __shfl_xor(sum, m);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = sum;
+        __syncthreads();
+        sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) sum += s_part[i];
+    }
+    const double inv = 1.0 / sqrt(sum / a.cols + double(a.eps));
+
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = threadIdx.x + c * NT;
+        const bool live = i < nvec;
+        const int64_t at = row * a.cols + i * 8;
+        if (live && a.residual_out) {
+            i32x4 o;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = int(pack_bf16(v[c][2 * q], v[c][2 * q + 1]));
+            *reinterpret_cast<i32x4*>(a.residual_out + at) = o;
+        }
+        i32x4 o;
+        float y[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float y0 = float(double(v[c][2 * q]) * inv * double(bf16_lo(w[c][q])));
+            const float y1 = float(double(v[c][2 * q + 1]) * inv * double(bf16_hi(w[c][q])));
+            o[q] = int(pack_bf16(y0, y1));
+            y[2 * q] = bf16_lo(o[q]);
+            y[2 * q + 1] = bf16_hi(o[q]);
+        }
+        if (live && a.y) *reinterpret_cast<i32x4*>(a.y + at) = o;
+        if constexpr (kQuant != 0) {
+            uint32_t lo, hi;
+            constexpr int kLanes = kQuant == 1 ? 16 : 4;
+            const float s = quant8<kLanes>(y, lo, hi);   // cols % group == 0: a group is live as a whole
+            if (live) {
+                *reinterpret_cast<uint2*>(a.codes + at) = uint2{lo, hi};
+                if ((threadIdx.x & (kLanes - 1)) == 0) {
+                    const int64_t g = at / (8 * kLanes);
+                    if constexpr (kQuant == 1) static_cast<float*>(a.scales)[g] = s;
+                    else static_cast<uint8_t*>(a.scales)[g] = uint8_t(__float_as_uint(s) >> 23);
+                }
+            }
+        }
+    }
+}
+
+template <int NT, int CH>
+hipError_t launch(const NormArgs& a, int quant, hipStream_t s) {
+    void (*kern)(NormArgs) = quant == 0 ? norm_kernel<NT, CH, 0>
+                             : quant == 1 ? norm_kernel<NT, CH, 1> : norm_kernel<NT, CH, 2>;
+    hipLaunchKernelGGL(kern, grid_of(a.rows), dim3(NT), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int norm_max_cols() { return 1024 * 8 * 4; }
+
+hipError_t launch_norm(const NormArgs& a, int quant, hipStream_t s) {
+    const int nvec = a.cols >> 3;
+    if (nvec <= 64) return launch<64, 1>(a, quant, s);
+    if (nvec <= 256) return launch<256, 1>(a, quant, s);
+    if (nvec <= 512) return launch<256, 2>(a, quant, s);
+    if (nvec <= 1024) return launch<256, 4>(a, quant, s);
+    if (nvec <= 2048) return launch<512, 4>(a, quant, s);
+    return launch<1024, 4>(a, quant, s);
+}
+
+}  // namespace moe
