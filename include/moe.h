@@ -484,14 +484,10 @@ MOE_API int moe_silu_mul(const void* h, int32_t rows, int32_t cols, float clamp_
  *   w        device, E4M3FN [N, K]
  *   w_scale  device, fp32 [ceil(N / 128), K / 128]
  *   out      device, bf16 [M, N]   (output; must not overlap an input)
- *   workspace  device, >= moe_gemm_fp8_workspace(M, N, K) bytes, 256-byte
- *              aligned; NULL when that is 0; contents on entry do not matter
  * Requires N >= 1, K % 128 == 0, 128 <= K <= 2^20 and M, N <= 2^30.
  */
-MOE_API int64_t moe_gemm_fp8_workspace(int32_t M, int32_t N, int32_t K);
 MOE_API int moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int32_t M,
-                         int32_t N, int32_t K, void* out, void* workspace, int64_t workspace_bytes,
-                         hipStream_t stream);
+                         int32_t N, int32_t K, void* out, hipStream_t stream);
 
 /*
  * moe_grouped_gemm — products of rows that are already sorted by expert, the

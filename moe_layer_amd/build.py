@@ -1,4 +1,5 @@
-"""Builds libmoe_mi355x.so in-tree with hipcc for gfx950.
+"""Builds libmoe_mi355x.so in-tree with hipcc for gfx950, and the Python
+side of its torch operators (_binding.so, host code only) with g++.
 
     python -m moe_layer_amd.build          # compile every source, link
 """
@@ -10,11 +11,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_mi355x.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -41,12 +44,31 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding():
+    import torch
+    tdir = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(tdir, "include"),
+           "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L", os.path.join(tdir, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding build failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = True) -> str:
-    """Compile every HIP source and link the shared library; returns its path."""
+    """Compile every HIP source and link the shared library, and build the
+    binding; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, srcs))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,6 +1,7 @@
 // Launchers and shared device code of the operators around the fused layer:
 // the quantising RMSNorm (norm.hip), the quantising SiLU-gated multiply
-// (act.hip) and the dense and grouped products (gemm_rows.hip).
+// (act.hip) and the dense and grouped products (gemm_pick.hip,
+// gemm_split.hip, gemm_tile.hip).
 #pragma once
 
 #include "common.h"
@@ -88,5 +89,8 @@ struct RowsGemmArgs {
     int rows, E, N, K;
 };
 hipError_t launch_rows_gemm(const RowsGemmArgs& g, bool fp8, hipStream_t s);
+// its two forms, `shape` one of gemm_pick.hip's tiles
+hipError_t launch_rows_split(const RowsGemmArgs& g, bool fp8, int shape, hipStream_t s);
+hipError_t launch_rows_tile(const RowsGemmArgs& g, bool fp8, int shape, hipStream_t s);
 
 }  // namespace moe

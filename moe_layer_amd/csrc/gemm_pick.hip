@@ -1,0 +1,74 @@
+// The tile a dense or grouped product runs in.
+//
+// Both forms (gemm_split.hip, gemm_tile.hip) are bound by the bytes a CU gets
+// from L2 into its LDS, 38-83 GB/s by tile, for most sizes: a workgroup of
+// BW x BT outputs fetches (BW + BT) 128-byte rows per K step, so large tiles
+// move fewer bytes and small ones fill the 256 CUs.  The time of a tile shape
+// is modelled as
+//   start + rounds (round + steps step),
+// rounds = workgroups / 256, rounded up, steps = K steps of 128 bytes, and at
+// least the bytes that have to come from HBM; the fastest shape is taken.  The
+// constants are a least-squares fit over 35 dense shapes from 1 x 512 x 512 to
+// 8192 x 4096 x 7168 (each shape timed in every tile; residual 3-16 %).  Over
+// those and 16 grouped ones the pick is 2.3 % slower than the best tile in the
+// geometric mean, 25 % at worst.
+#include <algorithm>
+#include <cmath>
+
+#include "dense.h"
+
+namespace moe {
+
+namespace {
+
+struct Tile {
+    bool split;        // gemm_split.hip, else gemm_tile.hip
+    int shape;         // its number there
+    int bw, bt;        // weight rows and token rows
+    float start, round, step;   // us
+};
+
+constexpr Tile kTiles[] = {
+    {true, 0, 16, 16, 1.14f, 1.10f, 0.0571f},    {true, 1, 32, 16, 1.05f, 1.23f, 0.0805f},
+    {true, 2, 32, 32, 0.87f, 1.48f, 0.1039f},    {true, 3, 64, 32, 0.64f, 1.95f, 0.1529f},
+    {true, 4, 64, 48, 0.42f, 2.61f, 0.1789f},    {true, 5, 64, 64, 0.33f, 3.07f, 0.2167f},
+    {true, 6, 64, 80, 0.17f, 3.66f, 0.2399f},    {true, 7, 128, 48, 0.44f, 3.60f, 0.2954f},
+    {false, 0, 64, 16, 3.52f, 0.11f, 0.1353f},   {false, 1, 128, 64, 4.14f, -0.17f, 0.4899f},
+    {false, 2, 128, 128, 0.48f, 2.89f, 0.6462f}, {false, 3, 256, 128, -0.10f, 4.25f, 1.0058f},
+    {false, 4, 256, 256, -4.67f, 9.42f, 1.5528f},
+};
+
+constexpr double kHbmBytesPerUs = 5.8e6;   // streaming reads and writes (6 TB/s reads alone)
+
+double time_us(const Tile& t, const RowsGemmArgs& g, bool fp8) {
+    const double es = fp8 ? 1 : 2, steps = g.K * es / 128;
+    const int64_t groups = g.offsets ? std::min(g.E, g.rows) : 1;
+    // row blocks: of a group's rows, known on the device only, the last one is
+    // half full on average
+    const double blocks = g.offsets ? std::max(double(groups), double(g.rows) / t.bt + 0.5 * groups)
+                                    : std::ceil(double(g.rows) / t.bt);
+    const double fill = blocks * ((g.N + t.bw - 1) / t.bw) / 256;
+    const double rounds = fill <= 4 ? std::ceil(fill) : fill + 0.5;
+    const double us = t.start + rounds * (t.round + steps * t.step);
+    const double bytes = (double(groups) * g.N + g.rows) * g.K * es + 2.0 * g.rows * g.N;
+    const double hbm = bytes / kHbmBytesPerUs;
+    // long streams overlap with the rest in part only
+    return hbm < 20 ? us : std::max(us, hbm) + 0.3 * std::min(us, hbm);
+}
+
+}  // namespace
+
+hipError_t launch_rows_gemm(const RowsGemmArgs& g, bool fp8, hipStream_t s) {
+    const Tile* best = nullptr;
+    double least = 0;
+    for (const Tile& t : kTiles) {
+        const double us = time_us(t, g, fp8);
+        if (!best || us < least) {
+            best = &t;
+            least = us;
+        }
+    }
+    return best->split ? launch_rows_split(g, fp8, best->shape, s) : launch_rows_tile(g, fp8, best->shape, s);
+}
+
+}  // namespace moe

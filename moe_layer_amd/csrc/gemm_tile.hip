@@ -1,0 +1,228 @@
+// LDS-tiled dense and grouped products (see gemm_split.hip for the products and
+// the operand sides).
+//
+// A workgroup owns BW weight rows x BT token rows of one group.  A stage is
+// 128 bytes of K of every row (128 e4m3 or 64 bf16 elements, one fp8 scale
+// block), moved global -> LDS with direct-to-LDS loads of 8 whole 128-byte row
+// pieces into an S-slot ring, S - 1 stages ahead; each wave waits for its own
+// loads, then one barrier per stage publishes the slot and frees the one read
+// before.  LDS rows are 128 bytes with chunk c of row r at position
+// c ^ (r & 7), so the 8 lanes that read 8 rows at one chunk hit all banks.
+//
+// fp8: a stage's products p are one 16x16x128 MFMA per 16 x 16 tile, folded
+// with acc += (a_scale w_scale) p; the scales of 8 stages at a time sit in a
+// two-slot LDS table that is filled along with the ring.
+#include "dev_rows.h"
+
+namespace moe {
+
+namespace {
+
+// Weight tiles that an XCD's workgroups of one time share with some row blocks
+// (8192 x 4096 x 7168 in 256 x 256 tiles: 2 / 4 / 8 / 16 tiles 231 / 227 / 224 / 229 us).
+constexpr int kBand = 4;
+
+template <bool FP8, int BW, int BT, int WW, int WT, int S, bool NTW>
+__global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g, int ntiles, int band) {
+    constexpr int W = WW * WT;
+    constexpr int SA = BW / WW / 16, SB = BT / WT / 16;      // 16-row subtiles per wave
+    constexpr int kPieces = (BW + BT) / 8;                   // 1 KB loads per stage
+    constexpr int NL = (kPieces + W - 1) / W;                // loads per wave per stage
+    constexpr int kSlot = (BW + BT) * 128;
+    constexpr int kScaleRows = FP8 ? (BT + (BW + 127) / 128 + 7) / 8 * 8 : 0;
+    constexpr int kTab = kScaleRows * 32;                    // 8 stages of fp32 scales per row
+    constexpr int kParts = (kScaleRows / 8 + W - 1) / W;     // table loads per wave per 8 stages
+    static_assert((BW / 8) % W == 0 && S >= 2 && S - 1 + kParts <= 8, "tile shape");
+    constexpr int kOut = BT * kOutRow<BW>;                   // the finished tile, in the ring's place
+    constexpr int kLds = S * kSlot + 2 * kTab > kOut ? S * kSlot + 2 * kTab : kOut;
+    static_assert(kLds <= 160 * 1024, "LDS");
+    // one LDS object: with several, the compiler waits for every direct-to-LDS
+    // load before each LDS read
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+    lds_t* const ring = (lds_t*)lds;
+    lds_t* const tab = ring + S * kSlot;
+
+    // item -> (band of weight tiles, row block, tile in the band): the items an
+    // XCD works on at a time share `band` weight tiles and some row blocks
+    const int slots = count_blocks<BT>(g);
+    int64_t item;
+    if (!xcd_item(int64_t(slots) * ntiles, item)) return;    // the whole workgroup alike
+    const int64_t per_band = int64_t(band) * slots;
+    const int b = int(item / per_band);
+    const int64_t in = item - b * per_band;
+    const int wide = min(band, ntiles - b * band);
+    const int slot = int(in / wide), tile = b * band + int(in % wide);
+    int e, row0, row1;
+    if (!find_block<BT>(g, slot, e, row0, row1)) return;
+
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wv % WW, wt = wv / WW;
+    const int lr = lane & 15, lk = lane >> 4;
+    const int64_t kbytes = int64_t(g.K) * (FP8 ? 1 : 2);
+    const int steps = int(kbytes >> 7);
+    const int n0 = tile * BW;
+
+    const uint8_t* wbase = g.w + (int64_t(e) * g.N + n0) * kbytes;
+    const uint8_t* abase = g.a + int64_t(row0) * kbytes;
+    uint32_t off[NL];                                        // this lane's bytes of each piece
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+        const int r = 8 * min(wv + W * j, kPieces - 1) + (lane >> 3);
+        const int src = j < BW / 8 / W ? min(r, g.N - 1 - n0) : min(r - BW, row1 - 1 - row0);
+        off[j] = uint32_t(src) * uint32_t(kbytes) + (((lane & 7) ^ (lane >> 3)) << 4);
+    }
+    auto issue = [&](int st) {
+        lds_t* to = ring + (st % S) * kSlot;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const uint8_t* base = (j < BW / 8 / W ? wbase : abase) + (int64_t(st) << 7);
+            load_piece<NTW>(base + off[j], to + min(wv + W * j, kPieces - 1) * 1024, j < BW / 8 / W);
+        }
+    };
+    // part p of the scales of stages 8 c .. 8 c + 7: one load of 8 table rows
+    auto issue_scales = [&](int c, int p) {
+        if constexpr (FP8) {
+            const int piece = min(wv + W * p, kScaleRows / 8 - 1);
+            const int r = 8 * piece + (lane >> 3);
+            const int nb = (g.N + 127) >> 7;
+            const int64_t row = r < BT ? min(row0 + r, row1 - 1)
+                                       : int64_t(e) * nb + min((n0 >> 7) + r - BT, nb - 1);
+            const float* src = (r < BT ? g.a_scale : g.w_scale) + row * steps + min(8 * c + (lane & 7), steps - 1);
+            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(src), tab + (c & 1) * kTab + piece * 256, 4,
+                                             0, 0);
+        }
+    };
+    // the loads of stage st; its chunk of 8 stages starts the next one's scales
+    // once the chunk before is out of use (S - 1 stages in)
+    auto issue_stage = [&](int st) {
+        if constexpr (FP8) {
+            const int p = (st & 7) - (S - 1);
+            if (p >= 0 && p < kParts && (st >> 3) * 8 + 8 < steps) issue_scales((st >> 3) + 1, p);
+        }
+        issue(st);
+    };
+
+    // fragment addresses
+    const uint32_t arow = uint32_t(wm * (BW / WW) + lr) * 128;
+    const uint32_t brow = uint32_t(BW + wt * (BT / WT) + lr) * 128;
+    const uint32_t c0 = uint32_t(lk ^ (lr & 7)) << 4, c1 = c0 ^ 64;
+
+    f32x4 acc[SA][SB];
+#pragma unroll
+    for (int i = 0; i < SA; ++i)
+#pragma unroll
+        for (int t = 0; t < SB; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+
+    auto fold = [](f32x4& to, float scale, const f32x4& p) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) to[q] = __builtin_fmaf(scale, p[q], to[q]);
+    };
+    f32x4 prev[SB];
+    float last_sc[SB];
+#pragma unroll
+    for (int t = 0; t < SB; ++t) {
+        prev[t] = f32x4{0, 0, 0, 0};
+        last_sc[t] = 0.0f;
+    }
+
+    if constexpr (FP8) {
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) issue_scales(0, p);
+    }
+    for (int st = 0; st < S - 1 && st < steps; ++st) issue_stage(st);
+    for (int s = 0; s < steps; ++s) {
+        // fewer loads than are in flight at most: the table's come before a stage's own
+        wait_stages<NL, S - 2>(min(s + S - 2, steps - 1) - s);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + S - 1 < steps) issue_stage(s + S - 1);
+        const lds_t* from = ring + (s % S) * kSlot;
+        i32x4 b0[SB], b1[SB];
+        float sc[SB];
+#pragma unroll
+        for (int t = 0; t < SB; ++t) {
+            b0[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c0);
+            b1[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c1);
+        }
+        if constexpr (FP8) {
+            const lds_t* row = tab + ((s >> 3) & 1) * kTab + (s & 7) * 4;
+            const float sw = *reinterpret_cast<lds_f*>(row + (BT + wm * (BW / WW) / 128) * 32);
+#pragma unroll
+            for (int t = 0; t < SB; ++t)
+                sc[t] = __fmul_rn(*reinterpret_cast<lds_f*>(row + (wt * (BT / WT) + 16 * t + lr) * 32), sw);
+        }
+        // subtile row i is multiplied while row i + 1 is read and row i - 1 (for
+        // i = 0 the last of the stage before) is folded
+        i32x4 a0 = *reinterpret_cast<lds_v4*>(from + arow + c0), a1 = *reinterpret_cast<lds_v4*>(from + arow + c1);
+#pragma unroll
+        for (int i = 0; i < SA; ++i) {
+            i32x4 n0, n1;
+            if (i + 1 < SA) {
+                n0 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c0);
+                n1 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c1);
+            }
+#pragma unroll
+            for (int t = 0; t < SB; ++t) {
+                if constexpr (FP8) {
+                    const f32x4 p = mma_step<true>(a0, a1, b0[t], b1[t], f32x4{0, 0, 0, 0});
+                    __builtin_amdgcn_sched_barrier(0);
+                    fold(acc[(i + SA - 1) % SA][t], i == 0 ? last_sc[t] : sc[t], prev[t]);
+                    prev[t] = p;
+                    __builtin_amdgcn_sched_barrier(0);
+                } else {
+                    acc[i][t] = mma_step<false>(a0, a1, b0[t], b1[t], acc[i][t]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            a0 = n0;
+            a1 = n1;
+        }
+#pragma unroll
+        for (int t = 0; t < SB; ++t) last_sc[t] = sc[t];
+    }
+    if constexpr (FP8) {
+#pragma unroll
+        for (int t = 0; t < SB; ++t) fold(acc[SA - 1][t], last_sc[t], prev[t]);
+    }
+    __syncthreads();                                         // the ring is idle: the outputs take its place
+#pragma unroll
+    for (int t = 0; t < SB; ++t)
+#pragma unroll
+        for (int i = 0; i < SA; ++i)
+            stage4<BW>(ring, wt * (BT / WT) + 16 * t + lr, wm * (BW / WW) + 16 * i + 4 * lk, acc[i][t]);
+    __syncthreads();
+    store_tile<BW, BT, 64 * W>(g, ring, row0, row1, n0);
+}
+
+template <bool FP8, int BW, int BT, int WW, int WT, int S>
+hipError_t launch_tile(const RowsGemmArgs& g, hipStream_t s) {
+    const int ntiles = (g.N + BW - 1) / BW;
+    const int64_t slots = block_slots(g, BT);
+    void (*kern)(RowsGemmArgs, int, int) = one_pass(g, BT, FP8)
+                                               ? rows_tile_kernel<FP8, BW, BT, WW, WT, S, true>
+                                               : rows_tile_kernel<FP8, BW, BT, WW, WT, S, false>;
+    hipLaunchKernelGGL(kern, xcd_grid(slots * ntiles), dim3(64 * WW * WT), 0, s, g, ntiles, std::min(kBand, ntiles));
+    return hipGetLastError();
+}
+
+template <bool FP8>
+hipError_t launch(const RowsGemmArgs& g, int shape, hipStream_t s) {
+    switch (shape) {
+        case 0: return launch_tile<FP8, 64, 16, 4, 1, 4>(g, s);
+        case 1: return launch_tile<FP8, 128, 64, 4, 1, 3>(g, s);
+        case 2: return launch_tile<FP8, 128, 128, 2, 4, 4>(g, s);
+        case 3: return launch_tile<FP8, 256, 128, 4, 2, 3>(g, s);
+        case 4: return launch_tile<FP8, 256, 256, 2, 4, 2>(g, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rows_tile(const RowsGemmArgs& g, bool fp8, int shape, hipStream_t s) {
+    return fp8 ? launch<true>(g, shape, s) : launch<false>(g, shape, s);
+}
+
+}  // namespace moe

@@ -120,18 +120,10 @@ MOE_API int moe_silu_mul(const void* h, int32_t rows, int32_t cols, float clamp_
                                       static_cast<uint16_t*>(y), codes, scales, stream));
 }
 
-MOE_API int64_t moe_gemm_fp8_workspace(int32_t M, int32_t N, int32_t K) {
-    if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
-    if (K % MOE_QUANT_GROUP != 0 || M > kMaxRows || N > kMaxRows || K > kMaxCols)
-        return MOE_ERR_UNSUPPORTED;
-    return 0;
-}
-
 MOE_API int moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int32_t M,
-                         int32_t N, int32_t K, void* out, void* workspace, int64_t workspace_bytes,
-                         hipStream_t stream) {
-    const int64_t need = moe_gemm_fp8_workspace(M, N, K);
-    if (need < 0) return int(need);
+                         int32_t N, int32_t K, void* out, hipStream_t stream) {
+    if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+    if (K % MOE_QUANT_GROUP != 0 || M > kMaxRows || N > kMaxRows || K > kMaxCols) return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;
     const int st = check_product(a, a_scale, w, w_scale, out, true);
     if (st != MOE_OK) return st;
@@ -139,7 +131,6 @@ MOE_API int moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* 
     if (clash({{out, 2 * int64_t(M) * N}},
               {{a, mk}, {a_scale, 4 * M * kb}, {w, nk}, {w_scale, 4 * ((int64_t(N) + 127) / 128) * kb}}, 0))
         return MOE_ERR_INVALID_ARG;
-    if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
     RowsGemmArgs g{};
     g.a = a;
     g.a_scale = a_scale;

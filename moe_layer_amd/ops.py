@@ -27,7 +27,7 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route", "moe_align_capacity"
            "moe_align_scratch_bytes", "moe_align_ws",
            "moe_quant_act", "moe_quant_act_mx", "moe_pack_mx_scales", "moe_plan", "moe_forward_workspace", "moe_forward",
            "moe_forward_profiled", "moe_decode_layer", "moe_forward_noalloc",
-           "moe_rmsnorm", "moe_silu_mul", "moe_gemm_fp8_workspace", "moe_gemm_fp8", "moe_grouped_gemm")
+           "moe_rmsnorm", "moe_silu_mul", "moe_gemm_fp8", "moe_grouped_gemm")
 MOE_NUM_STAGES = 5
 MOE_NOALLOC_MAX_BYTES = 64 << 20
 MOE_SYNC_WORDS, MOE_SYNC_ERROR = 640, 576
@@ -102,10 +102,8 @@ def lib() -> C.CDLL:
         L.moe_rmsnorm.argtypes = [vp, vp, vp, C.c_float, i32, i32, i32, vp, vp, vp, vp, vp]
         L.moe_silu_mul.restype = C.c_int
         L.moe_silu_mul.argtypes = [vp, i32, i32, C.c_float, i32, vp, vp, vp, vp]
-        L.moe_gemm_fp8_workspace.restype = i64
-        L.moe_gemm_fp8_workspace.argtypes = [i32, i32, i32]
         L.moe_gemm_fp8.restype = C.c_int
-        L.moe_gemm_fp8.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, i64, vp]
+        L.moe_gemm_fp8.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp]
         L.moe_grouped_gemm.restype = C.c_int
         L.moe_grouped_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
         _lib = L
@@ -404,47 +402,49 @@ def moe_decode_layer(x, w13, w2, topk_ids=None, topk_weights=None, w13_scale=Non
 
 
 # ---- operators around the layer ---------------------------------------------
+# Their argument checks and output allocation are native too (csrc/binding.cpp):
+# one of these calls takes as long as the kernel it launches when it serves a
+# single token.
 
 _QUANT = {None: MOE_WDTYPE_BF16, "fp8": MOE_WDTYPE_FP8_E4M3, "mxfp8": MOE_WDTYPE_MXFP8}
-_FP8 = (torch.float8_e4m3fn, torch.uint8)
+_native = None
 
 
-def _on(fn, name, dev, *args):
-    """Call a library entry on ``dev``'s current stream, with ``dev`` current."""
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+def _binding():
+    global _native
+    if _native is None:
+        try:
+            from . import _binding as m
+        except ImportError as e:
+            raise RuntimeError("the package's native binding is missing or does not load: build it with "
+                               "`python -m moe_layer_amd.build`") from e
+        L = lib()
+        m.bind(*(C.cast(f, C.c_void_p).value for f in (L.moe_rmsnorm, L.moe_silu_mul, L.moe_gemm_fp8,
+                                                       L.moe_grouped_gemm)))
+        _native = m
+    return _native
+
+
+def _call(name: str, first: torch.Tensor, *args):
+    """A native entry on the current stream of ``first``'s device, with that
+    device current."""
+    f = getattr(_native or _binding(), name)
+    i = first.get_device()
+    if i < 0:                        # not on a GPU: the checks refuse it before anything is launched
+        r = f(first, *args, 0)
+    elif i == torch._C._cuda_getDevice():
+        r = f(first, *args, torch._C._cuda_getCurrentRawStream(i))
     else:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    if st != MOE_OK:
-        raise MoeError(name, st)
+        with torch.cuda.device(i):
+            r = f(first, *args, torch._C._cuda_getCurrentRawStream(i))
+    if type(r) is int:
+        raise MoeError("moe_" + name, r)
+    return r
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _is(t, dtypes, shape, dev, what):
-    """Check one tensor argument: its type, shape, layout and device."""
-    assert t.dtype in dtypes, f"{what}: dtype {t.dtype}, expected one of {dtypes}"
-    assert t.shape == shape, f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}"
-    assert t.is_contiguous(), f"{what}: must be contiguous"
-    assert t.device == dev, f"{what}: on {t.device}, expected {dev}"
-
-
-def _codes(rows, cols, quant, dev, codes, scales):
-    """The code and scale tensors of a quantised output, allocated when not given."""
-    group = MOE_QUANT_GROUP if quant == "fp8" else MOE_MX_BLOCK
-    stype = torch.float32 if quant == "fp8" else torch.uint8
-    if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    else:
-        _is(codes, _FP8, (rows, cols), dev, "codes")
-    if scales is None:
-        scales = torch.empty((rows, max(cols // group, 1)), dtype=stype, device=dev)
-    else:
-        _is(scales, (stype,), (rows, max(cols // group, 1)), dev, "scales")
-    return codes, scales
+def _quant(quant) -> int:
+    assert quant in _QUANT, f"quant: {quant!r}, expected None, 'fp8' or 'mxfp8'"
+    return _QUANT[quant]
 
 
 def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None, quant=None, with_y=None,
@@ -452,38 +452,11 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     """Residual addition + RMSNorm of bf16 rows [rows, cols], quantised on the
     way when ``quant`` is "fp8" (codes + fp32 scales per 128 columns, what
     moe_quant_act makes of y) or "mxfp8" (E8M0 bytes per 32, moe_quant_act_mx).
-    ``with_y``: whether the bf16 row is written too (default: only without
-    ``quant``).  y and residual_out may be x or residual themselves.  Returns
-    (y, residual_out, codes, scales), None for what was not asked for."""
-    assert quant in _QUANT, f"quant: {quant!r}, expected None, 'fp8' or 'mxfp8'"
-    assert x.dim() == 2, "x: [rows, cols]"
-    rows, cols = x.shape
-    dev, bf16 = x.device, (torch.bfloat16,)
-    _is(x, bf16, (rows, cols), dev, "x")
-    _is(weight, bf16, (cols,), dev, "weight")
-    if with_y is None:
-        with_y = y is not None or quant is None
-    if not with_y:
-        assert y is None, "y given with with_y=False"
-    elif y is None:
-        y = torch.empty_like(x)
-    else:
-        _is(y, bf16, (rows, cols), dev, "y")
-    if residual is None:
-        assert residual_out is None, "residual_out needs a residual"
-    else:
-        _is(residual, bf16, (rows, cols), dev, "residual")
-        if residual_out is None:
-            residual_out = torch.empty_like(x)
-        else:
-            _is(residual_out, bf16, (rows, cols), dev, "residual_out")
-    if quant is None:
-        assert codes is None and scales is None, "codes and scales need quant"
-    else:
-        codes, scales = _codes(rows, cols, quant, dev, codes, scales)
-    _on(lib().moe_rmsnorm, "moe_rmsnorm", dev, _addr(x), _addr(residual), _addr(weight), eps, rows, cols,
-        _QUANT[quant], _addr(residual_out), _addr(y), _addr(codes), _addr(scales))
-    return y, residual_out, codes, scales
+    ``with_y``: whether the bf16 row is written too (default: when y is given
+    or there is no ``quant``).  y and residual_out may be x or residual
+    themselves.  Outputs that are not given are allocated.  Returns (y,
+    residual_out, codes, scales), None for what was not asked for."""
+    return _call("rmsnorm", x, weight, eps, residual, _quant(quant), with_y, y, residual_out, codes, scales)
 
 
 def moe_silu_mul(h: torch.Tensor, quant=None, clamp_limit: float = 0.0, with_y=None, y=None, codes=None, scales=None):
@@ -491,57 +464,15 @@ def moe_silu_mul(h: torch.Tensor, quant=None, clamp_limit: float = 0.0, with_y=N
     with the fused layer's rounding points and clamp, quantised on the way as
     moe_rmsnorm does.  Returns (y, codes, scales), None for what was not asked
     for."""
-    assert quant in _QUANT, f"quant: {quant!r}, expected None, 'fp8' or 'mxfp8'"
-    assert h.dim() == 2 and h.shape[1] % 2 == 0, "h: [rows, 2 * cols]"
-    rows, cols = h.shape[0], h.shape[1] // 2
-    dev, bf16 = h.device, (torch.bfloat16,)
-    _is(h, bf16, (rows, 2 * cols), dev, "h")
-    if with_y is None:
-        with_y = y is not None or quant is None
-    if not with_y:
-        assert y is None, "y given with with_y=False"
-    elif y is None:
-        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    else:
-        _is(y, bf16, (rows, cols), dev, "y")
-    if quant is None:
-        assert codes is None and scales is None, "codes and scales need quant"
-    else:
-        codes, scales = _codes(rows, cols, quant, dev, codes, scales)
-    _on(lib().moe_silu_mul, "moe_silu_mul", dev, _addr(h), rows, cols, clamp_limit, _QUANT[quant], _addr(y),
-        _addr(codes), _addr(scales))
-    return y, codes, scales
+    return _call("silu_mul", h, _quant(quant), clamp_limit, with_y, y, codes, scales)
 
 
-def moe_gemm_fp8_workspace(M: int, N: int, K: int) -> int:
-    n = lib().moe_gemm_fp8_workspace(M, N, K)
-    if n < 0:
-        raise MoeError("moe_gemm_fp8_workspace", int(n))
-    return int(n)
-
-
-def moe_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, out=None,
-                 workspace=None) -> torch.Tensor:
+def moe_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                 out=None) -> torch.Tensor:
     """Dense product of quantised rows and block-scaled weights: e4m3 a [M, K]
     with fp32 a_scale [M, K/128], e4m3 w [N, K] with fp32 w_scale
     [ceil(N/128), K/128]; returns bf16 out [M, N]."""
-    assert a.dim() == 2 and w.dim() == 2, "a: [M, K], w: [N, K]"
-    (M, K), N, dev = a.shape, w.shape[0], a.device
-    kb, f32 = K // MOE_QUANT_GROUP, (torch.float32,)
-    _is(a, _FP8, (M, K), dev, "a")
-    _is(w, _FP8, (N, K), dev, "w")
-    _is(a_scale, f32, (M, kb), dev, "a_scale")
-    _is(w_scale, f32, (-(-N // 128), kb), dev, "w_scale")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    else:
-        _is(out, (torch.bfloat16,), (M, N), dev, "out")
-    need = moe_gemm_fp8_workspace(M, N, K)
-    if need and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _on(lib().moe_gemm_fp8, "moe_gemm_fp8", dev, _addr(a), _addr(a_scale), _addr(w), _addr(w_scale), M, N, K,
-        _addr(out), _addr(workspace) if need else None, workspace.numel() if need else 0)
-    return out
+    return _call("gemm_fp8", a, a_scale, w, w_scale, out)
 
 
 def moe_grouped_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, a_scale=None, w_scale=None,
@@ -551,23 +482,4 @@ def moe_grouped_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, a_
     or e4m3 ones with fp32 a_scale [rows, K/128] and w_scale [E, ceil(N/128),
     K/128].  Returns bf16 out [rows, N]; rows outside every group keep what
     out held (uninitialised when it is allocated here)."""
-    assert a.dim() == 2 and w.dim() == 3, "a: [rows, K], w: [E, N, K]"
-    (rows, K), (E, N), dev = a.shape, w.shape[:2], a.device
-    fp8 = a.dtype in _FP8
-    types = _FP8 if fp8 else (torch.bfloat16,)
-    _is(a, types, (rows, K), dev, "a")
-    _is(w, types, (E, N, K), dev, "w")
-    _is(offsets, (torch.int32,), (E + 1,), dev, "offsets")
-    if fp8:
-        assert a_scale is not None and w_scale is not None, "fp8 operands need a_scale and w_scale"
-        _is(a_scale, (torch.float32,), (rows, K // MOE_QUANT_GROUP), dev, "a_scale")
-        _is(w_scale, (torch.float32,), (E, -(-N // 128), K // MOE_QUANT_GROUP), dev, "w_scale")
-    else:
-        assert a_scale is None and w_scale is None, "bf16 operands take no scales"
-    if out is None:
-        out = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
-    else:
-        _is(out, (torch.bfloat16,), (rows, N), dev, "out")
-    _on(lib().moe_grouped_gemm, "moe_grouped_gemm", dev, _addr(a), _addr(a_scale), _addr(w), _addr(w_scale),
-        _addr(offsets), rows, E, N, K, MOE_WDTYPE_FP8_E4M3 if fp8 else MOE_WDTYPE_BF16, _addr(out))
-    return out
+    return _call("grouped_gemm", a, w, offsets, a_scale, w_scale, out)

@@ -160,9 +160,9 @@ def pow2(rng, shape, lo, hi):
 
 def exact_operands(rng, rows, E, N, K, fp8):
     """Operands whose every partial sum is an exact fp32 value: |a| <= 7 and
-    |w| <= 15, scales from four neighbouring powers of two, so a sum is below
-    2^7 K 2^6 of its smallest unit (K <= 2^11)."""
-    assert K <= 2048
+    |w| <= 15, scales from four neighbouring powers of two on either side, so a
+    sum is at most 105 K 2^6 of its smallest unit, below 2^24 for K <= 2304."""
+    assert 105 * K * 64 < 2 ** 24
     nb = -(-N // 128)
     if fp8:
         a, w = small_fp8(rng, (rows, K), 7), small_fp8(rng, (E, N, K), 15)
@@ -206,7 +206,9 @@ def put(*ts):
 DENSE = [(1, 1, 128), (1, 16, 256), (2, 3, 128), (15, 17, 384), (16, 128, 2048), (17, 130, 256), (33, 200, 640),
          (64, 576, 512), (65, 64, 1024), (100, 4096, 128), (127, 257, 256), (128, 256, 384), (129, 255, 128),
          (255, 300, 512), (256, 512, 256), (300, 129, 1152), (513, 640, 256), (1000, 264, 384), (1, 4096, 2048),
-         (40, 1000, 2048), (700, 1031, 256), (2, 20000, 128)]
+         (40, 1000, 2048), (700, 1031, 256), (2, 20000, 128), (243, 4315, 256), (324, 2712, 256), (300, 4096, 2304),
+         (770, 4741, 128), (1358, 1030, 384), (194, 4424, 128), (1500, 2001, 2304), (2177, 2737, 128),
+         (1100, 5003, 1280), (3905, 3217, 128), (2300, 4100, 2304)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -271,6 +273,29 @@ def test_grouped_gemm(sizes, head, tail, N, K, fp8):
         second = out.clone()
         ops.moe_grouped_gemm(ad, wd, offd, sad, swd, out=second)
         assert same_bits(second, out)
+
+
+# rows in groups of uneven sizes (some empty), N, K: the larger tiles, and weights too many for the last-level cache
+TILES = [(1083, 2, 103, 384), (4202, 2, 79, 128), (5939, 16, 87, 256), (5683, 3, 137, 256), (955, 40, 390, 256),
+         (748, 40, 474, 1280), (59, 16, 1341, 384), (1358, 40, 783, 128), (5449, 3, 129, 384), (3747, 40, 1156, 128),
+         (4763, 5, 2601, 128), (4815, 40, 1288, 640), (40, 32, 4096, 1024), (700, 32, 4096, 1024)]
+
+
+@pytest.mark.parametrize("rows,E,N,K", TILES)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_grouped_gemm_tiles(rows, E, N, K, fp8):
+    rng = np.random.default_rng(rows + E)
+    load = rng.exponential(size=E) ** 2
+    off = sizes_to_offsets(rng.multinomial(rows, load / load.sum()))
+    a, w, sa, sw, av, wv = exact_operands(rng, rows, E, N, K, fp8)
+    ref = O.grouped_product(av, wv, off)
+    ad, wd, sad, swd = put(a, w, sa, sw)
+    buf = torch.full((rows + 2, N), 5.0, dtype=torch.bfloat16, device=dev())
+    # an output that starts inside a buffer where its rows are whole 16-byte pieces
+    out = buf[1: rows + 1] if (2 * N) % 16 == 0 else buf[:rows]
+    ops.moe_grouped_gemm(ad, wd, torch.from_numpy(off).to(dev()), sad, swd, out=out)
+    np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(ref))
+    assert (buf[rows + 1:] == 5.0).all() and (out.data_ptr() == buf.data_ptr() or (buf[0] == 5.0).all())
 
 
 @pytest.mark.parametrize("fp8", [False, True])
