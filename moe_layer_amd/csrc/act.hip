@@ -20,16 +20,15 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// silu(g) to about 2^-22 relative, without overflow on either side:
-// z = exp(-|g|) = 2^n 2^f with n whole and |f| <= 1/2 (the product |g| log2(e)
-// split in two parts, so f keeps its low bits), r = 1 / (1 + z) with one
-// Newton step, silu = g r for g >= 0 and g r z else.
+// silu(g) without overflow on either side: z = exp(-|g|) = 2^n 2^f with n whole
+// and |f| <= 1/2 (f from an fma, so it keeps its low bits), r = 1 / (1 + z)
+// with one Newton step, silu = g r for g >= 0 and g r z else.  Without the
+// Newton step one of the 65280 finite gates (5.9375) rounds to the wrong bf16.
 __device__ __forceinline__ float silu_f32(float g) {
     constexpr float kL = 1.44269504088896341f;             // log2(e) rounded to fp32
-    constexpr float kLlo = 1.92596299112661746887e-8f;     // log2(e) - kL
     const float a = fminf(__builtin_fabsf(g), 1000.0f);    // z and silu(-a) are 0 long before
     const float n = __builtin_rintf(a * -kL);
-    const float f = __builtin_fmaf(-a, kLlo, __builtin_fmaf(-a, kL, -n));
+    const float f = __builtin_fmaf(-a, kL, -n);
     const float ex = __builtin_amdgcn_exp2f(f);
     const int ni = int(n);
     const float d = __fadd_rn(1.0f, __builtin_amdgcn_ldexpf(ex, ni));
@@ -43,14 +42,15 @@ __global__ __launch_bounds__(kThreads) void silu_mul_kernel(const uint16_t* __re
                                                            float limit, uint16_t* __restrict__ yout,
                                                            uint8_t* __restrict__ codes, void* __restrict__ scales) {
     const int per_row = cols >> 3;
-    const int64_t i = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-    const bool live = i < int64_t(rows) * per_row;   // a quantisation group is live as a whole
-    const int64_t row = live ? i / per_row : 0;
-    const int col = live ? int(i - row * per_row) * 8 : 0;
-    const uint16_t* src = h + row * 2 * cols + col;
+    const int64_t total = int64_t(rows) * per_row;
+    const int64_t mine = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+    const bool live = mine < total;                  // a quantisation group is live as a whole
+    const int64_t i = min(mine, total - 1);
+    const int64_t at = i * 8;                        // first output column, over all rows
+    const uint16_t* src = h + at + i / per_row * cols;
     const i32x4 gw = *reinterpret_cast<const i32x4*>(src);
     const i32x4 uw = *reinterpret_cast<const i32x4*>(src + cols);
-    float g[8], u[8], y[8];
+    float g[8], u[8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         g[2 * q] = bf16_lo(gw[q]);
@@ -70,20 +70,18 @@ __global__ __launch_bounds__(kThreads) void silu_mul_kernel(const uint16_t* __re
     for (int q = 0; q < 4; ++q) {
         const uint32_t sl = pack_bf16(silu_f32(g[2 * q]), silu_f32(g[2 * q + 1]));
         o[q] = int(pack_bf16(__fmul_rn(bf16_lo(sl), u[2 * q]), __fmul_rn(bf16_hi(sl), u[2 * q + 1])));
-        y[2 * q] = bf16_lo(o[q]);
-        y[2 * q + 1] = bf16_hi(o[q]);
     }
-    if (live && yout) *reinterpret_cast<i32x4*>(yout + row * cols + col) = o;
+    if (live && yout) *reinterpret_cast<i32x4*>(yout + at) = o;
     if constexpr (kQuant != 0) {
         constexpr int kLanes = kQuant == 1 ? 16 : 4;
         uint32_t lo, hi;
-        const float s = quant8<kLanes>(y, lo, hi);
+        const float s = quant8<kLanes>(o, lo, hi);
         if (live) {
-            *reinterpret_cast<uint2*>(codes + row * cols + col) = uint2{lo, hi};
+            *reinterpret_cast<uint2*>(codes + at) = uint2{lo, hi};
             if ((threadIdx.x & (kLanes - 1)) == 0) {
-                const int64_t at = (row * cols + col) / (8 * kLanes);
-                if constexpr (kQuant == 1) static_cast<float*>(scales)[at] = s;
-                else static_cast<uint8_t*>(scales)[at] = uint8_t(__float_as_uint(s) >> 23);
+                const int64_t group = at / (8 * kLanes);
+                if constexpr (kQuant == 1) static_cast<float*>(scales)[group] = s;
+                else static_cast<uint8_t*>(scales)[group] = uint8_t(__float_as_uint(s) >> 23);
             }
         }
     }
@@ -96,8 +94,8 @@ hipError_t launch_silu_mul(const uint16_t* h, int rows, int cols, float clamp_li
     const int64_t n = int64_t(rows) * (cols >> 3);
     void (*kern)(const uint16_t*, int, int, float, uint16_t*, uint8_t*, void*) =
         quant == 0 ? silu_mul_kernel<0> : quant == 1 ? silu_mul_kernel<1> : silu_mul_kernel<2>;
-    hipLaunchKernelGGL(kern, grid_of((n + kThreads - 1) / kThreads), dim3(kThreads), 0, s, h, rows, cols, clamp_limit, y, codes,
-                       scales);
+    hipLaunchKernelGGL(kern, grid_of((n + kThreads - 1) / kThreads), dim3(kThreads), 0, s, h, rows, cols, clamp_limit,
+                       y, codes, scales);
     return hipGetLastError();
 }
 

@@ -29,22 +29,42 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Codes and scale of 8 consecutive bf16 values of a quantisation group held by
-// `kLanes` neighbouring lanes (16: a 128-column group, 4: a 32-column one),
-// which call it together: moe_quant_act's rule.  Returns the scale.
+// maximum of the two 16-bit halves of each word
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+    typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max_u16(uint32_t v) {
+    return pk_max_u16(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, false)));
+}
+
+// Codes and scale of 8 consecutive bf16 values (packed, w) of a quantisation
+// group held by kLanes neighbouring lanes (16: a 128-column group, 4: a
+// 32-column one), which call it together: moe_quant_act's rule, whose scale
+// never saturates a finite value.  The maximum is taken over the bits without
+// their sign, which order as the magnitudes do.  Returns the scale.
 template <int kLanes>
-__device__ __forceinline__ float quant8(const float (&v)[8], uint32_t& lo, uint32_t& hi) {
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, __builtin_fabsf(v[i]));
-#pragma unroll
-    for (int m = 1; m < kLanes; m <<= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
-    const float s = fp8_group_scale(amax);
+__device__ __forceinline__ float quant8(const i32x4& w, uint32_t& lo, uint32_t& hi) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    uint32_t m = pk_max_u16(pk_max_u16(uint32_t(w[0]) & kAbs, uint32_t(w[1]) & kAbs),
+                            pk_max_u16(uint32_t(w[2]) & kAbs, uint32_t(w[3]) & kAbs));
+    m = dpp_max_u16<0xb1>(m);                              // quad_perm [1,0,3,2]
+    m = dpp_max_u16<0x4e>(m);                              // quad_perm [2,3,0,1]
+    if constexpr (kLanes == 16) {
+        m = dpp_max_u16<0x141>(m);                         // row_half_mirror
+        m = dpp_max_u16<0x140>(m);                         // row_mirror
+    }
+    const float s = fp8_group_scale(__uint_as_float(max(m & 0xffffu, m >> 16) << 16));
     // 1 / s of a power of two: mirror the exponent (s >= 2^-42, so 1 / s is normal)
     const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(__fmul_rn(v[i], inv), -448.0f), 448.0f);
+    for (int i = 0; i < 4; ++i) {
+        q[2 * i] = __fmul_rn(bf16_lo(w[i]), inv);
+        q[2 * i + 1] = __fmul_rn(bf16_hi(w[i]), inv);
+    }
     lo = pack_e4m3(q[0], q[1], q[2], q[3]);
     hi = pack_e4m3(q[4], q[5], q[6], q[7]);
     return s;

@@ -1,17 +1,17 @@
 // The tile a dense or grouped product runs in.
 //
 // Both forms (gemm_split.hip, gemm_tile.hip) are bound by the bytes a CU gets
-// from L2 into its LDS, 38-83 GB/s by tile, for most sizes: a workgroup of
+// from L2 into its LDS, 58-86 GB/s by tile, for most sizes: a workgroup of
 // BW x BT outputs fetches (BW + BT) 128-byte rows per K step, so large tiles
 // move fewer bytes and small ones fill the 256 CUs.  The time of a tile shape
 // is modelled as
 //   start + rounds (round + steps step),
 // rounds = workgroups / 256, rounded up, steps = K steps of 128 bytes, and at
 // least the bytes that have to come from HBM; the fastest shape is taken.  The
-// constants are a least-squares fit over 35 dense shapes from 1 x 512 x 512 to
-// 8192 x 4096 x 7168 (each shape timed in every tile; residual 3-16 %).  Over
-// those and 16 grouped ones the pick is 2.3 % slower than the best tile in the
-// geometric mean, 25 % at worst.
+// constants are a least-squares fit over 61 dense shapes from 1 x 512 x 512 to
+// 8192 x 2112 x 7168, each timed in every tile (residual 7-16 %, 256 x 256
+// tiles 24 %).  Over those and 27 grouped ones the pick is 1.4 % slower than
+// the best tile in the geometric mean, 17 % at worst.
 #include <algorithm>
 #include <cmath>
 
@@ -25,17 +25,18 @@ struct Tile {
     bool split;        // gemm_split.hip, else gemm_tile.hip
     int shape;         // its number there
     int bw, bt;        // weight rows and token rows
+    int pair;          // 2 where two workgroups or more fit a CU's LDS, else 1
     float start, round, step;   // us
 };
 
 constexpr Tile kTiles[] = {
-    {true, 0, 16, 16, 1.14f, 1.10f, 0.0571f},    {true, 1, 32, 16, 1.05f, 1.23f, 0.0805f},
-    {true, 2, 32, 32, 0.87f, 1.48f, 0.1039f},    {true, 3, 64, 32, 0.64f, 1.95f, 0.1529f},
-    {true, 4, 64, 48, 0.42f, 2.61f, 0.1789f},    {true, 5, 64, 64, 0.33f, 3.07f, 0.2167f},
-    {true, 6, 64, 80, 0.17f, 3.66f, 0.2399f},    {true, 7, 128, 48, 0.44f, 3.60f, 0.2954f},
-    {false, 0, 64, 16, 3.52f, 0.11f, 0.1353f},   {false, 1, 128, 64, 4.14f, -0.17f, 0.4899f},
-    {false, 2, 128, 128, 0.48f, 2.89f, 0.6462f}, {false, 3, 256, 128, -0.10f, 4.25f, 1.0058f},
-    {false, 4, 256, 256, -4.67f, 9.42f, 1.5528f},
+    {true, 0, 16, 16, 1, 1.18f, 1.14f, 0.0561f},    {true, 1, 32, 16, 1, 1.10f, 1.27f, 0.0830f},
+    {true, 2, 32, 32, 1, 0.95f, 1.49f, 0.1069f},    {true, 3, 64, 32, 1, 0.83f, 1.91f, 0.1562f},
+    {true, 4, 64, 48, 1, 0.68f, 2.53f, 0.1813f},    {true, 5, 64, 64, 1, 0.59f, 2.97f, 0.2185f},
+    {true, 6, 64, 80, 1, 0.49f, 3.54f, 0.2398f},    {true, 7, 128, 48, 1, 0.68f, 3.77f, 0.2805f},
+    {false, 0, 64, 16, 2, 2.81f, 0.36f, 0.1193f},   {false, 1, 128, 64, 2, 3.05f, 0.70f, 0.4237f},
+    {false, 2, 128, 128, 1, 0.43f, 3.22f, 0.4740f}, {false, 3, 256, 128, 1, -0.55f, 5.00f, 0.7345f},
+    {false, 4, 256, 256, 1, -3.14f, 8.62f, 1.0621f},
 };
 
 constexpr double kHbmBytesPerUs = 5.8e6;   // streaming reads and writes (6 TB/s reads alone)
@@ -52,8 +53,8 @@ double time_us(const Tile& t, const RowsGemmArgs& g, bool fp8) {
     const double us = t.start + rounds * (t.round + steps * t.step);
     const double bytes = (double(groups) * g.N + g.rows) * g.K * es + 2.0 * g.rows * g.N;
     const double hbm = bytes / kHbmBytesPerUs;
-    // long streams overlap with the rest in part only
-    return hbm < 20 ? us : std::max(us, hbm) + 0.3 * std::min(us, hbm);
+    // long streams overlap with the rest in part only, better so where a CU has two workgroups
+    return hbm < 20 ? us : std::max(us, hbm) + 0.3 / t.pair * std::min(us, hbm);
 }
 
 }  // namespace

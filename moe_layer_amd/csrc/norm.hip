@@ -74,20 +74,17 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
             *reinterpret_cast<i32x4*>(a.residual_out + at) = o;
         }
         i32x4 o;
-        float y[8];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float y0 = float(double(v[c][2 * q]) * inv * double(bf16_lo(w[c][q])));
             const float y1 = float(double(v[c][2 * q + 1]) * inv * double(bf16_hi(w[c][q])));
             o[q] = int(pack_bf16(y0, y1));
-            y[2 * q] = bf16_lo(o[q]);
-            y[2 * q + 1] = bf16_hi(o[q]);
         }
         if (live && a.y) *reinterpret_cast<i32x4*>(a.y + at) = o;
         if constexpr (kQuant != 0) {
             uint32_t lo, hi;
             constexpr int kLanes = kQuant == 1 ? 16 : 4;
-            const float s = quant8<kLanes>(y, lo, hi);   // cols % group == 0: a group is live as a whole
+            const float s = quant8<kLanes>(o, lo, hi);   // cols % group == 0: a group is live as a whole
             if (live) {
                 *reinterpret_cast<uint2*>(a.codes + at) = uint2{lo, hi};
                 if ((threadIdx.x & (kLanes - 1)) == 0) {

@@ -208,7 +208,7 @@ DENSE = [(1, 1, 128), (1, 16, 256), (2, 3, 128), (15, 17, 384), (16, 128, 2048),
          (255, 300, 512), (256, 512, 256), (300, 129, 1152), (513, 640, 256), (1000, 264, 384), (1, 4096, 2048),
          (40, 1000, 2048), (700, 1031, 256), (2, 20000, 128), (243, 4315, 256), (324, 2712, 256), (300, 4096, 2304),
          (770, 4741, 128), (1358, 1030, 384), (194, 4424, 128), (1500, 2001, 2304), (2177, 2737, 128),
-         (1100, 5003, 1280), (3905, 3217, 128), (2300, 4100, 2304)]
+         (1100, 5003, 1280), (3905, 3217, 128), (2300, 4100, 2304), (254, 4287, 640), (36, 4187, 1536)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -278,7 +278,8 @@ def test_grouped_gemm(sizes, head, tail, N, K, fp8):
 # rows in groups of uneven sizes (some empty), N, K: the larger tiles, and weights too many for the last-level cache
 TILES = [(1083, 2, 103, 384), (4202, 2, 79, 128), (5939, 16, 87, 256), (5683, 3, 137, 256), (955, 40, 390, 256),
          (748, 40, 474, 1280), (59, 16, 1341, 384), (1358, 40, 783, 128), (5449, 3, 129, 384), (3747, 40, 1156, 128),
-         (4763, 5, 2601, 128), (4815, 40, 1288, 640), (40, 32, 4096, 1024), (700, 32, 4096, 1024)]
+         (4763, 5, 2601, 128), (4815, 40, 1288, 640), (2995, 40, 391, 2304), (5247, 40, 150, 256),
+         (852, 40, 398, 512), (40, 32, 4096, 1024), (700, 32, 4096, 1024)]
 
 
 @pytest.mark.parametrize("rows,E,N,K", TILES)
