@@ -94,9 +94,8 @@ hipError_t launch_silu_mul(const uint16_t* h, int rows, int cols, float clamp_li
     const int64_t n = int64_t(rows) * (cols >> 3);
     void (*kern)(const uint16_t*, int, int, float, uint16_t*, uint8_t*, void*) =
         quant == 0 ? silu_mul_kernel<0> : quant == 1 ? silu_mul_kernel<1> : silu_mul_kernel<2>;
-    hipLaunchKernelGGL(kern, grid_of((n + kThreads - 1) / kThreads), dim3(kThreads), 0, s, h, rows, cols, clamp_limit,
-                       y, codes, scales);
-    return hipGetLastError();
+    return start(kern, grid_of((n + kThreads - 1) / kThreads), kThreads, s, h, rows, cols, clamp_limit, y, codes,
+                 scales);
 }
 
 }  // namespace moe

@@ -70,6 +70,17 @@ __device__ __forceinline__ float quant8(const i32x4& w, uint32_t& lo, uint32_t& 
     return s;
 }
 
+// Launch one kernel with its arguments (what <<<>>> does, in one runtime call
+// instead of three; these launches stand between kernels of a few us).
+template <typename... P, typename... A>
+hipError_t start(void (*kern)(P...), dim3 grid, int threads, hipStream_t s, A... args) {
+    static_assert(sizeof...(P) == sizeof...(A), "kernel arguments");
+    return [&](P... p) {
+        void* list[] = {static_cast<void*>(&p)...};
+        return hipLaunchKernel(reinterpret_cast<const void*>(kern), grid, dim3(threads), list, 0, s);
+    }(args...);
+}
+
 // A grid of at least n workgroups (n >= 1) numbered blockIdx.y * gridDim.x +
 // blockIdx.x: a grid dimension holds less than 2^32 threads.
 inline dim3 grid_of(int64_t n) {

@@ -170,8 +170,7 @@ hipError_t launch_split(const RowsGemmArgs& g, hipStream_t s) {
     const int64_t slots = block_slots(g, BT);
     void (*kern)(RowsGemmArgs, int, int) = one_pass(g, BT, FP8) ? rows_split_kernel<FP8, BW, BT, W, D, true>
                                                                       : rows_split_kernel<FP8, BW, BT, W, D, false>;
-    hipLaunchKernelGGL(kern, grid_of(slots * ntiles), dim3(64 * W), 0, s, g, ntiles, int(slots));
-    return hipGetLastError();
+    return start(kern, grid_of(slots * ntiles), 64 * W, s, g, ntiles, int(slots));
 }
 
 template <bool FP8>

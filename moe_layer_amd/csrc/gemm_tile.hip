@@ -230,8 +230,7 @@ hipError_t launch_tile(const RowsGemmArgs& g, hipStream_t s) {
     void (*kern)(RowsGemmArgs, int, int) = one_pass(g, BT, FP8)
                                                ? rows_tile_kernel<FP8, BW, BT, WW, WT, S, true>
                                                : rows_tile_kernel<FP8, BW, BT, WW, WT, S, false>;
-    hipLaunchKernelGGL(kern, xcd_grid(slots * ntiles), dim3(64 * WW * WT), 0, s, g, ntiles, std::min(kBand, ntiles));
-    return hipGetLastError();
+    return start(kern, xcd_grid(slots * ntiles), 64 * WW * WT, s, g, ntiles, std::min(kBand, ntiles));
 }
 
 template <bool FP8>

@@ -101,8 +101,7 @@ template <int NT, int CH>
 hipError_t launch(const NormArgs& a, int quant, hipStream_t s) {
     void (*kern)(NormArgs) = quant == 0 ? norm_kernel<NT, CH, 0>
                              : quant == 1 ? norm_kernel<NT, CH, 1> : norm_kernel<NT, CH, 2>;
-    hipLaunchKernelGGL(kern, grid_of(a.rows), dim3(NT), 0, s, a);
-    return hipGetLastError();
+    return start(kern, grid_of(a.rows), NT, s, a);
 }
 
 }  // namespace

@@ -408,6 +408,7 @@ def moe_decode_layer(x, w13, w2, topk_ids=None, topk_weights=None, w13_scale=Non
 
 _QUANT = {None: MOE_WDTYPE_BF16, "fp8": MOE_WDTYPE_FP8_E4M3, "mxfp8": MOE_WDTYPE_MXFP8}
 _native = None
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _binding():
@@ -432,11 +433,11 @@ def _call(name: str, first: torch.Tensor, *args):
     i = first.get_device()
     if i < 0:                        # not on a GPU: the checks refuse it before anything is launched
         r = f(first, *args, 0)
-    elif i == torch._C._cuda_getDevice():
-        r = f(first, *args, torch._C._cuda_getCurrentRawStream(i))
+    elif i == _current_device():
+        r = f(first, *args, _raw_stream(i))
     else:
         with torch.cuda.device(i):
-            r = f(first, *args, torch._C._cuda_getCurrentRawStream(i))
+            r = f(first, *args, _raw_stream(i))
     if type(r) is int:
         raise MoeError("moe_" + name, r)
     return r
