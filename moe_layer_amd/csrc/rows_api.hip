@@ -129,7 +129,7 @@ MOE_API int moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* 
     if (st != MOE_OK) return st;
     const int64_t mk = int64_t(M) * K, nk = int64_t(N) * K, kb = K / MOE_QUANT_GROUP;
     if (clash({{out, 2 * int64_t(M) * N}},
-              {{a, mk}, {a_scale, 4 * M * kb}, {w, nk}, {w_scale, 4 * ((int64_t(N) + 127) / 128) * kb}}, 0))
+              {{a, mk}, {a_scale, 4 * kb * M}, {w, nk}, {w_scale, 4 * ((int64_t(N) + 127) / 128) * kb}}, 0))
         return MOE_ERR_INVALID_ARG;
     RowsGemmArgs g{};
     g.a = a;
@@ -160,7 +160,7 @@ MOE_API int moe_grouped_gemm(const void* a, const float* a_scale, const void* w,
     if (!offsets || !aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
     const int64_t es = fp8 ? 1 : 2, kb = K / MOE_QUANT_GROUP, nb = (int64_t(N) + 127) / 128;
     if (clash({{out, 2 * int64_t(rows) * N}},
-              {{a, es * rows * K}, {a_scale, 4 * rows * kb}, {w, es * E * N * K}, {w_scale, 4 * E * nb * kb},
+              {{a, es * rows * K}, {a_scale, 4 * kb * rows}, {w, es * E * N * K}, {w_scale, 4 * kb * nb * E},
                {offsets, 4 * (int64_t(E) + 1)}}, 0))
         return MOE_ERR_INVALID_ARG;
     RowsGemmArgs g{};

@@ -299,6 +299,17 @@ def test_grouped_gemm_tiles(rows, E, N, K, fp8):
     assert (buf[rows + 1:] == 5.0).all() and (out.data_ptr() == buf.data_ptr() or (buf[0] == 5.0).all())
 
 
+@pytest.mark.parametrize("K", [64, 192, 320])
+def test_grouped_bf16_odd_steps(K):
+    """K in whole 64-element steps that are no multiple of 128."""
+    rng = np.random.default_rng(K)
+    sizes = [3, 0, 40, 17]
+    off = sizes_to_offsets(sizes)
+    a, w, _, _, av, wv = exact_operands(rng, sum(sizes), len(sizes), 72, K, False)
+    out = ops.moe_grouped_gemm(*put(a, w, torch.from_numpy(off)))
+    np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(O.grouped_product(av, wv, off)))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("off", [[-5, 3, 7, 400], [10, 4, 90, 60], [0, 1000, 1000, 2000], [120, 120, 120, 120]])
 def test_grouped_bad_offsets_stay_in_bounds(off, fp8):
@@ -335,6 +346,67 @@ def test_grouped_rows_do_not_depend_on_their_neighbours(fp8):
     keep[[69, 71]] = False
     assert torch.equal(got[keep].view(torch.int16), clean[keep].view(torch.int16))
     assert got[69].isnan().all()
+
+
+def test_beyond_32_bits():
+    """Buffers past 2^32 elements: the last rows of large inputs, weights and
+    outputs, with everything in front of them zero (or not looked at)."""
+    d = dev()
+    last = 3
+    g = torch.Generator().manual_seed(32)
+    # rows of x, h, codes and outputs past 2^32 elements
+    rows, cols = 2 ** 32 // 8192 + 1029, 8192
+    tail = rng_bf16(g, last, cols)
+    w = rng_bf16(g, cols)
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=d)
+    x[-last:] = tail.to(d)
+    y, _, codes, scales = ops.moe_rmsnorm(x, w.to(d), 1e-6, quant="fp8", y=x)     # in place, to save memory
+    yo, _ = O.rmsnorm(bf16_to_f64(tail), None, bf16_to_f64(w), 1e-6)
+    np.testing.assert_array_equal(bf16_to_f64(y[-last:]), yo)
+    check_codes("fp8", y[-last:].contiguous(), codes[-last:], scales[-last:])
+    assert not y[:-last].any()
+    a, c2, s2 = ops.moe_silu_mul(x, quant="mxfp8", with_y=True)
+    ao = O.silu_mul(yo)
+    np.testing.assert_array_equal(bf16_to_f64(a[-last:]), ao)
+    check_codes("mxfp8", a[-last:].contiguous(), c2[-last:], s2[-last:])
+    del y, a, c2, s2
+    # the codes as rows of a product: a past 2^32 bytes
+    rng = np.random.default_rng(33)
+    _, wq, _, sw, _, wv = exact_operands(rng, 1, 2, 40, 2304, True)
+    wq, sw, wv = wq[:, :, :256].contiguous(), sw[:, :, :2].contiguous(), wv[:, :, :256]
+    big = codes.view(-1, 256)                     # more rows of fewer columns
+    n = big.shape[0]
+    scale = torch.ones(n, 2, dtype=torch.float32, device=d)
+    off = torch.tensor([5, n - 70, n], dtype=torch.int32, device=d)
+    av = O.act_values(big[-70:].cpu().numpy(), np.ones((70, 2)))
+    ref = av @ wv[1].T
+    wqd, swd = put(wq, sw)
+    out = ops.moe_grouped_gemm(big, wqd, off, scale, swd)
+    assert (np.abs(bf16_to_f64(out[-70:]) - ref) <= tolerance(av, wv[1], ref, True)).all()
+    out = ops.moe_gemm_fp8(big, scale, wqd[1].contiguous(), swd[1].contiguous())
+    assert (np.abs(bf16_to_f64(out[-70:]) - ref) <= tolerance(av, wv[1], ref, True)).all()
+    del x, codes, scales, big, scale, out
+    # outputs past 2^32 elements, and weights past 2^32 bytes
+    rows, N, K = 2 ** 32 // 4096 + 517, 4096, 128
+    ab = torch.zeros(rows, K, dtype=torch.bfloat16, device=d)
+    tail, wide = rng_bf16(g, 300, K), rng_bf16(g, 1, N, K)
+    ab[-300:] = tail.to(d)
+    out = ops.moe_grouped_gemm(ab, wide.to(d), torch.tensor([0, rows], dtype=torch.int32, device=d))
+    av, wv = bf16_to_f64(tail), bf16_to_f64(wide)
+    ref = av @ wv[0].T
+    assert (np.abs(bf16_to_f64(out[-300:]) - ref) <= tolerance(av, wv[0], ref, False)).all()
+    del out, ab
+    E, N, K = 300, 4096, 2048
+    wl = torch.zeros(E, N, K, dtype=torch.bfloat16, device=d)
+    one = rng_bf16(g, N, K)
+    wl[-1] = one.to(d)
+    at = rng_bf16(g, 20, K)
+    sizes = [0] * (E - 2) + [4, 16]
+    out = ops.moe_grouped_gemm(at.to(d), wl, torch.from_numpy(sizes_to_offsets(sizes)).to(d))
+    av, wv = bf16_to_f64(at[4:]), bf16_to_f64(one)
+    ref = av @ wv.T
+    assert (np.abs(bf16_to_f64(out[4:]) - ref) <= tolerance(av, wv, ref, False)).all()
+    assert not out[:4].any()
 
 
 # ------------------------------------------------- together, as a user would ---
