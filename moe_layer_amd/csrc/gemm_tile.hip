@@ -22,38 +22,34 @@ namespace {
 // (8192 x 4096 x 7168 in 256 x 256 tiles: 2 / 4 / 8 / 16 tiles 231 / 227 / 224 / 229 us).
 constexpr int kBand = 4;
 
+// Bytes of LDS: the ring and the scale table's two slots, or the finished tile in their place
+template <bool FP8, int BW, int BT, int S>
+constexpr int tile_lds() {
+    const int rows = FP8 ? (BT + (BW + 127) / 128 + 7) / 8 * 8 : 0;
+    return std::max(S * (BW + BT) * 128 + 2 * rows * 32, BT * kOutRow<BW>);
+}
+
+// One tile: weight rows n0 .. n0 + BW - 1 against rows row0 .. min(row0 + BT, row1) - 1 of group e
 template <bool FP8, int BW, int BT, int WW, int WT, int S, bool NTW>
-__global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g, int ntiles, int band) {
+__device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring, int e, int row0, int row1, int n0) {
     constexpr int W = WW * WT;
     constexpr int SA = BW / WW / 16, SB = BT / WT / 16;      // 16-row subtiles per wave
     constexpr int kPieces = (BW + BT) / 8;                   // 1 KB loads per stage
     constexpr int NL = (kPieces + W - 1) / W;                // loads per wave per stage
     constexpr int kSlot = (BW + BT) * 128;
+    // A ring of two, bf16: every wave has the tokens in registers by the first
+    // subtile row and half of its weight rows half-way through the stage, so a
+    // second barrier there lets three quarters of the stage after next start
+    // (32768 x 4096 x 1536, 128 groups 589 -> 575 us).  fp8 stages hold as much
+    // arithmetic behind more registers and do not gain (8192 x 4096 x 7168 208 / 213 us).
+    constexpr bool kEarly = !FP8 && S == 2;
+    constexpr int kHalf0 = NL - BW / 16 / W;                 // its loads of half 0
+    static_assert(!kEarly || 2 * 8 * W == BW / WW, "halves of a wave's weight rows");
     constexpr int kScaleRows = FP8 ? (BT + (BW + 127) / 128 + 7) / 8 * 8 : 0;
     constexpr int kTab = kScaleRows * 32;                    // 8 stages of fp32 scales per row
     constexpr int kParts = (kScaleRows / 8 + W - 1) / W;     // table loads per wave per 8 stages
     static_assert((BW / 8) % W == 0 && S >= 2 && S - 1 + kParts <= 8, "tile shape");
-    constexpr int kOut = BT * kOutRow<BW>;                   // the finished tile, in the ring's place
-    constexpr int kLds = S * kSlot + 2 * kTab > kOut ? S * kSlot + 2 * kTab : kOut;
-    static_assert(kLds <= 160 * 1024, "LDS");
-    // one LDS object: with several, the compiler waits for every direct-to-LDS
-    // load before each LDS read
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
-    lds_t* const ring = (lds_t*)lds;
     lds_t* const tab = ring + S * kSlot;
-
-    // item -> (band of weight tiles, row block, tile in the band): the items an
-    // XCD works on at a time share `band` weight tiles and some row blocks
-    const int slots = count_blocks<BT>(g);
-    int64_t item;
-    if (!xcd_item(int64_t(slots) * ntiles, item)) return;    // the whole workgroup alike
-    const int64_t per_band = int64_t(band) * slots;
-    const int b = int(item / per_band);
-    const int64_t in = item - b * per_band;
-    const int wide = min(band, ntiles - b * band);
-    const int slot = int(in / wide), tile = b * band + int(in % wide);
-    int e, row0, row1;
-    if (!find_block<BT>(g, slot, e, row0, row1)) return;
 
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -61,7 +57,6 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
     const int lr = lane & 15, lk = lane >> 4;
     const int64_t kbytes = int64_t(g.K) * (FP8 ? 1 : 2);
     const int steps = int(kbytes >> 7);
-    const int n0 = tile * BW;
 
     const uint8_t* wbase = g.w + (int64_t(e) * g.N + n0) * kbytes;
     const uint8_t* abase = g.a + int64_t(row0) * kbytes;
@@ -76,19 +71,17 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
         const uint8_t* base = (j < BW / 8 / W ? wbase : abase) + (int64_t(st) << 7);
         load_piece<NTW>(base + off[j], ring + (st % S) * kSlot + min(wv + W * j, kPieces - 1) * 1024, j < BW / 8 / W);
     };
-    // with one stage in flight every load is waited for, and a part block's
-    // missing rows need none
-    const bool part = S == 2 && row1 - row0 < BT;
-    auto issue = [&](int st) {
-        if (!part) {
+    // pieces of half 0: the tokens and the first half of each wave's weight rows; of half 1: the rest
+    auto half_of = [](int j) { return j < BW / 8 / W ? j & 1 : 0; };
+    auto issue = [&](int st, int half) {
 #pragma unroll
-            for (int j = 0; j < NL; ++j) load(st, j);
-        } else {
-#pragma unroll
-            for (int j = 0; j < NL; ++j)
-                if (j < BW / 8 / W || 8 * (wv + W * j) - BW < row1 - row0) load(st, j);
-        }
+        for (int j = 0; j < NL; ++j)
+            if (half < 0 || half == half_of(j)) load(st, j);
     };
+    // held in scalars: a lane's choice between two kernel arguments would be a
+    // load of its own, and its wait one for every load in flight
+    const float *a_scale = g.a_scale, *w_scale = g.w_scale;
+    asm("" : "+s"(a_scale), "+s"(w_scale));
     // part p of the scales of stages 8 c .. 8 c + 7: one load of 8 table rows
     auto issue_scales = [&](int c, int p) {
         if constexpr (FP8) {
@@ -97,19 +90,34 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
             const int nb = (g.N + 127) >> 7;
             const int64_t row = r < BT ? min(row0 + r, row1 - 1)
                                        : int64_t(e) * nb + min((n0 >> 7) + r - BT, nb - 1);
-            const float* src = (r < BT ? g.a_scale : g.w_scale) + row * steps + min(8 * c + (lane & 7), steps - 1);
+            const float* src = (r < BT ? a_scale : w_scale) + row * steps + min(8 * c + (lane & 7), steps - 1);
             __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(src), tab + (c & 1) * kTab + piece * 256, 4,
                                              0, 0);
         }
     };
     // the loads of stage st; its chunk of 8 stages starts the next one's scales
     // once the chunk before is out of use (S - 1 stages in)
-    auto issue_stage = [&](int st) {
+    auto issue_stage = [&](int st, int half) {
         if constexpr (FP8) {
             const int p = (st & 7) - (S - 1);
-            if (p >= 0 && p < kParts && (st >> 3) * 8 + 8 < steps) issue_scales((st >> 3) + 1, p);
+            if (half != 0 && p >= 0 && p < kParts && (st >> 3) * 8 + 8 < steps) issue_scales((st >> 3) + 1, p);
         }
-        issue(st);
+        issue(st, half);
+    };
+    // stage s has landed; fewer loads than are in flight at most: the table's
+    // come before a stage's own
+    auto wait_stage = [&](int s) {
+        if constexpr (!kEarly) wait_stages<NL, S - 2>(min(s + S - 2, steps - 1) - s);
+        else if (s + 1 < steps) wait_vm<kHalf0>();
+        else wait_vm<0>();
+    };
+    auto issue_at_start = [&](int s) {
+        if (s + S - 1 < steps) issue_stage(s + S - 1, kEarly ? 1 : -1);
+    };
+    // half-way through stage s every wave has read the tokens and half 0 of the weights
+    auto issue_half_way = [&](int s) {
+        barrier();
+        issue_stage(s + S, 0);
     };
 
     // fragment addresses
@@ -139,22 +147,23 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
 #pragma unroll
         for (int p = 0; p < kParts; ++p) issue_scales(0, p);
     }
-    for (int st = 0; st < S - 1 && st < steps; ++st) issue_stage(st);
+    for (int st = 0; st < S - 1 && st < steps; ++st) issue_stage(st, -1);
+    if (kEarly && S - 1 < steps) issue_stage(S - 1, 0);
     // a wave whose tokens or weight rows all lie past the end only loads
     const bool idle = wt * (BT / WT) >= row1 - row0 || n0 + wm * (BW / WW) >= g.N;
     for (int s = 0; idle && s < steps; ++s) {
-        wait_stages<NL, S - 2>(min(s + S - 2, steps - 1) - s);
+        wait_stage(s);
         barrier();
-        if (s + S - 1 < steps) issue_stage(s + S - 1);
+        issue_at_start(s);
+        if (kEarly && s + S < steps) issue_half_way(s);
     }
-    for (int s = 0; !idle && s < steps; ++s) {
-        // fewer loads than are in flight at most: the table's come before a stage's own
-        wait_stages<NL, S - 2>(min(s + S - 2, steps - 1) - s);
+    auto stage = [&](int s, auto half_way) {
+        wait_stage(s);
         barrier();
         // fp8: behind the first reads (1024 x 4096 x 4096 24.2 -> 23.2 us); the
         // bf16 stages, shorter in K, need their loads as early as can be (grouped
         // 32768 x 4096 x 1536 600 against 616 us)
-        if (!FP8 && s + S - 1 < steps) issue_stage(s + S - 1);
+        if (!FP8) issue_at_start(s);
         const lds_t* from = ring + (s % S) * kSlot;
         // The first product needs one subtile of each operand: those are read
         // first.  Subtile row i is multiplied while row i + 1 is read, behind the
@@ -169,8 +178,8 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
             b1[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c1);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (FP8 && s + S - 1 < steps) {
-            issue_stage(s + S - 1);
+        if (FP8) {
+            issue_at_start(s);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -185,6 +194,10 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
                 if (t == 0 && i + 1 < SA) {
                     n0 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c0);
                     n1 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c1);
+                }
+                if (half_way.value && t == 0 && i == SA / 2) {
+                    issue_half_way(s);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 if constexpr (FP8) {
                     if (t == 0 && i == 0) {
@@ -208,7 +221,13 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
         }
 #pragma unroll
         for (int t = 0; t < SB; ++t) last_sc[t] = sc[t];
-    }
+    };
+    // a branch in the middle of a stage would spill (fp8): the last two stages,
+    // which start no third, are their own loop
+    const int mine = idle ? 0 : steps;
+    int s = 0;
+    for (; kEarly && s + S < mine; ++s) stage(s, std::bool_constant<kEarly>());
+    for (; s < mine; ++s) stage(s, std::false_type());
     if constexpr (FP8) {
 #pragma unroll
         for (int t = 0; t < SB; ++t) fold(acc[SA - 1][t], last_sc[t], prev[t]);
@@ -221,6 +240,43 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
             stage4<BW>(ring, wt * (BT / WT) + 16 * t + lr, wm * (BW / WW) + 16 * i + 4 * lk, acc[i][t]);
     __syncthreads();
     store_tile<BW, BT, 64 * W>(g, ring, row0, row1, n0);
+}
+
+template <bool FP8, int BW, int BT, int WW, int WT, int S, bool NTW>
+__global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g, int ntiles, int band) {
+    // The last block of a group, of half the rows or fewer: the room of the
+    // missing ones goes into a third slot and all waves share the rest (20000
+    // rows in 64 bf16 groups of 2000 x 1024 120 -> 115 us, fp8 32768 x 4096 x
+    // 1536 in 128 351 -> 339 us).
+    constexpr bool kPart64 = BW == 256, kPart128 = BW == 256 && BT == 256;
+    constexpr int kLds = std::max({tile_lds<FP8, BW, BT, S>(), kPart64 ? tile_lds<FP8, BW, 64, 3>() : 0,
+                                   kPart128 ? tile_lds<FP8, BW, 128, 3>() : 0});
+    // one LDS object: with several, the compiler waits for every direct-to-LDS
+    // load before each LDS read
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+    static_assert(kLds <= 160 * 1024, "LDS");
+    lds_t* const ring = (lds_t*)lds;
+
+    // item -> (band of weight tiles, row block, tile in the band): the items an
+    // XCD works on at a time share `band` weight tiles and some row blocks
+    const int slots = count_blocks<BT>(g);
+    int64_t item;
+    if (!xcd_item(int64_t(slots) * ntiles, item)) return;    // the whole workgroup alike
+    const int64_t per_band = int64_t(band) * slots;
+    const int b = int(item / per_band);
+    const int64_t in = item - b * per_band;
+    const int wide = min(band, ntiles - b * band);
+    const int slot = int(in / wide), n0 = (b * band + int(in % wide)) * BW;
+    int e, row0, row1;
+    if (!find_block<BT>(g, slot, e, row0, row1)) return;
+
+    if constexpr (kPart64) {
+        if (row1 - row0 <= 64) return tile_product<FP8, BW, 64, 4, 2, 3, NTW>(g, ring, e, row0, row1, n0);
+    }
+    if constexpr (kPart128) {
+        if (row1 - row0 <= 128) return tile_product<FP8, BW, 128, 4, 2, 3, NTW>(g, ring, e, row0, row1, n0);
+    }
+    tile_product<FP8, BW, BT, WW, WT, S, NTW>(g, ring, e, row0, row1, n0);
 }
 
 template <bool FP8, int BW, int BT, int WW, int WT, int S>
