@@ -134,24 +134,31 @@ __device__ __forceinline__ void stage4(lds_t* tile, int t, int n, const f32x4& v
         i32x2{int(pack_bf16(v[0], v[1])), int(pack_bf16(v[2], v[3]))};
 }
 
-// V outputs per lane, V * 2 bytes aligned in every row (N % V == 0)
-template <int BW, int BT, int THREADS, int V, typename T>
+// V outputs per lane, V * 2 bytes aligned in every row (N % V == 0), by THREADS
+// neighbouring lanes.  NT: past the caches' replacement (tile_product).
+template <int BW, int BT, int THREADS, bool NT, int V, typename T>
 __device__ __forceinline__ void store_rows(const RowsGemmArgs& g, const lds_t* tile, int row0, int row1, int n0) {
     typedef const __attribute__((address_space(3))) T lds_T;
-    constexpr int kPer = BW / V;
+    constexpr int kPer = BW / V, kTurns = (BT * kPer + THREADS - 1) / THREADS;
     const int live = min(BT, row1 - row0);
-    for (int i = threadIdx.x; i < live * kPer; i += THREADS) {
+    // several pieces read ahead of their stores
+#pragma unroll(kTurns < 8 ? kTurns : 4)
+    for (int q = 0; q < kTurns; ++q) {
+        const int i = threadIdx.x % THREADS + q * THREADS;
         const int r = i / kPer, c = (i % kPer) * V;
-        if (n0 + c < g.N)
-            *reinterpret_cast<T*>(g.out + int64_t(row0 + r) * g.N + n0 + c) =
-                *reinterpret_cast<lds_T*>(tile + r * kOutRow<BW> + 2 * c);
+        if (r < live && n0 + c < g.N) {
+            const T v = *reinterpret_cast<lds_T*>(tile + r * kOutRow<BW> + 2 * c);
+            T* const to = reinterpret_cast<T*>(g.out + int64_t(row0 + r) * g.N + n0 + c);
+            if constexpr (NT) __builtin_nontemporal_store(v, to);
+            else *to = v;
+        }
     }
 }
-template <int BW, int BT, int THREADS>
+template <int BW, int BT, int THREADS, bool NT>
 __device__ __forceinline__ void store_tile(const RowsGemmArgs& g, const lds_t* tile, int row0, int row1, int n0) {
-    if ((g.N & 7) == 0) store_rows<BW, BT, THREADS, 8, i32x4>(g, tile, row0, row1, n0);
-    else if ((g.N & 1) == 0) store_rows<BW, BT, THREADS, 2, uint32_t>(g, tile, row0, row1, n0);
-    else store_rows<BW, BT, THREADS, 1, uint16_t>(g, tile, row0, row1, n0);
+    if ((g.N & 7) == 0) store_rows<BW, BT, THREADS, NT, 8, i32x4>(g, tile, row0, row1, n0);
+    else if ((g.N & 1) == 0) store_rows<BW, BT, THREADS, NT, 2, uint32_t>(g, tile, row0, row1, n0);
+    else store_rows<BW, BT, THREADS, NT, 1, uint16_t>(g, tile, row0, row1, n0);
 }
 
 template <bool FP8>

@@ -161,7 +161,7 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
         if (j < SA * SB) stage4<BW>((lds_t*)lds, 16 * (j % SB) + lr, 16 * (j / SB) + 4 * lk, v[q]);
     }
     __syncthreads();
-    store_tile<BW, BT, 64 * W>(g, (lds_t*)lds, row0, row1, n0);
+    store_tile<BW, BT, 64 * W, false>(g, (lds_t*)lds, row0, row1, n0);
 }
 
 template <bool FP8, int BW, int BT, int W, int D>

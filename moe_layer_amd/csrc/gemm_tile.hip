@@ -22,11 +22,11 @@ namespace {
 // (8192 x 4096 x 7168 in 256 x 256 tiles: 2 / 4 / 8 / 16 tiles 231 / 227 / 224 / 229 us).
 constexpr int kBand = 4;
 
-// Bytes of LDS: the ring and the scale table's two slots, or the finished tile in their place
+// Bytes of LDS: the ring and the scale table's two slots
 template <bool FP8, int BW, int BT, int S>
 constexpr int tile_lds() {
     const int rows = FP8 ? (BT + (BW + 127) / 128 + 7) / 8 * 8 : 0;
-    return std::max(S * (BW + BT) * 128 + 2 * rows * 32, BT * kOutRow<BW>);
+    return S * (BW + BT) * 128 + 2 * rows * 32;
 }
 
 // One tile: weight rows n0 .. n0 + BW - 1 against rows row0 .. min(row0 + BT, row1) - 1 of group e
@@ -49,6 +49,7 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     constexpr int kTab = kScaleRows * 32;                    // 8 stages of fp32 scales per row
     constexpr int kParts = (kScaleRows / 8 + W - 1) / W;     // table loads per wave per 8 stages
     static_assert((BW / 8) % W == 0 && S >= 2 && S - 1 + kParts <= 8, "tile shape");
+    static_assert(W * 16 * kOutRow<BW / WW> <= S * kSlot, "outputs in the ring's place");
     lds_t* const tab = ring + S * kSlot;
 
     const int lane = threadIdx.x & 63;
@@ -232,14 +233,24 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
 #pragma unroll
         for (int t = 0; t < SB; ++t) fold(acc[SA - 1][t], last_sc[t], prev[t]);
     }
-    __syncthreads();                                         // the ring is idle: the outputs take its place
-#pragma unroll
-    for (int t = 0; t < SB; ++t)
-#pragma unroll
-        for (int i = 0; i < SA; ++i)
-            stage4<BW>(ring, wt * (BT / WT) + 16 * t + lr, wm * (BW / WW) + 16 * i + 4 * lk, acc[i][t]);
+    // The ring is idle: each wave's outputs pass through 16 rows of its own, as
+    // it needs no other wave.  The stores of 256 weight rows, long streams for
+    // the most part, are past the caches' replacement: 32768 x 4096 x 1536 in 128
+    // groups 574 -> 550 us, and 635 -> 623 us with moe_silu_mul reading the
+    // result; 8192 x 4096 x 7168 213 -> 207 us, 228 -> 227 us with the reader.
     __syncthreads();
-    store_tile<BW, BT, 64 * W>(g, ring, row0, row1, n0);
+    constexpr int kCols = BW / WW;
+    lds_t* const rows16 = ring + wv * (16 * kOutRow<kCols>);
+#pragma unroll
+    for (int t = 0; t < SB; ++t) {
+#pragma unroll
+        for (int i = 0; i < SA; ++i) stage4<kCols>(rows16, lr, 16 * i + 4 * lk, acc[i][t]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        store_tile<kCols, 16, 64, BW == 256>(g, rows16, row0 + wt * (BT / WT) + 16 * t, row1, n0 + wm * kCols);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 template <bool FP8, int BW, int BT, int WW, int WT, int S, bool NTW>
