@@ -9,9 +9,10 @@
 // rounds = workgroups / 256, rounded up, steps = K steps of 128 bytes, and at
 // least the bytes that have to come from HBM; the fastest shape is taken.  The
 // constants are a least-squares fit over 61 dense shapes from 1 x 512 x 512 to
-// 8192 x 2112 x 7168, each timed in every tile (residual 7-16 %, 256 x 256
-// tiles 24 %).  Over those and 27 grouped ones the pick is 1.4 % slower than
-// the best tile in the geometric mean, 17 % at worst.
+// 8192 x 2112 x 7168, each timed in every tile (those of 256 weight rows where
+// there are more than 128 token rows; residual 7-14 %).  Over those and 27
+// grouped ones the pick is 1.4 % slower than the best tile in the geometric
+// mean, 18 % at worst.
 #include <algorithm>
 #include <cmath>
 
@@ -25,18 +26,17 @@ struct Tile {
     bool split;        // gemm_split.hip, else gemm_tile.hip
     int shape;         // its number there
     int bw, bt;        // weight rows and token rows
-    int pair;          // 2 where two workgroups or more fit a CU's LDS, else 1
     float start, round, step;   // us
 };
 
 constexpr Tile kTiles[] = {
-    {true, 0, 16, 16, 1, 1.18f, 1.14f, 0.0561f},    {true, 1, 32, 16, 1, 1.10f, 1.27f, 0.0830f},
-    {true, 2, 32, 32, 1, 0.95f, 1.49f, 0.1069f},    {true, 3, 64, 32, 1, 0.83f, 1.91f, 0.1562f},
-    {true, 4, 64, 48, 1, 0.68f, 2.53f, 0.1813f},    {true, 5, 64, 64, 1, 0.59f, 2.97f, 0.2185f},
-    {true, 6, 64, 80, 1, 0.49f, 3.54f, 0.2398f},    {true, 7, 128, 48, 1, 0.68f, 3.77f, 0.2805f},
-    {false, 0, 64, 16, 2, 2.81f, 0.36f, 0.1193f},   {false, 1, 128, 64, 2, 3.05f, 0.70f, 0.4237f},
-    {false, 2, 128, 128, 1, 0.43f, 3.22f, 0.4740f}, {false, 3, 256, 128, 1, -0.55f, 5.00f, 0.7345f},
-    {false, 4, 256, 256, 1, -3.14f, 8.62f, 1.0621f},
+    {true, 0, 16, 16, 1.18f, 1.14f, 0.0561f},    {true, 1, 32, 16, 1.10f, 1.27f, 0.0830f},
+    {true, 2, 32, 32, 0.95f, 1.49f, 0.1069f},    {true, 3, 64, 32, 0.83f, 1.91f, 0.1562f},
+    {true, 4, 64, 48, 0.68f, 2.53f, 0.1813f},    {true, 5, 64, 64, 0.59f, 2.97f, 0.2185f},
+    {true, 6, 64, 80, 0.49f, 3.54f, 0.2398f},    {true, 7, 128, 48, 0.68f, 3.77f, 0.2805f},
+    {false, 0, 64, 16, 2.53f, 0.34f, 0.1219f},   {false, 1, 128, 64, 2.66f, 0.79f, 0.4171f},
+    {false, 2, 128, 128, 0.20f, 3.07f, 0.4869f}, {false, 3, 256, 128, 0.48f, 4.37f, 0.8250f},
+    {false, 4, 256, 256, -1.06f, 7.37f, 1.3169f},
 };
 
 constexpr double kHbmBytesPerUs = 5.8e6;   // streaming reads and writes (6 TB/s reads alone)
@@ -53,8 +53,8 @@ double time_us(const Tile& t, const RowsGemmArgs& g, bool fp8) {
     const double us = t.start + rounds * (t.round + steps * t.step);
     const double bytes = (double(groups) * g.N + g.rows) * g.K * es + 2.0 * g.rows * g.N;
     const double hbm = bytes / kHbmBytesPerUs;
-    // long streams overlap with the rest in part only, better so where a CU has two workgroups
-    return hbm < 20 ? us : std::max(us, hbm) + 0.3 / t.pair * std::min(us, hbm);
+    // long streams overlap with the rest in part only
+    return hbm < 20 ? us : std::max(us, hbm) + 0.3 * std::min(us, hbm);
 }
 
 }  // namespace

@@ -279,7 +279,8 @@ def test_grouped_gemm(sizes, head, tail, N, K, fp8):
 TILES = [(1083, 2, 103, 384), (4202, 2, 79, 128), (5939, 16, 87, 256), (5683, 3, 137, 256), (955, 40, 390, 256),
          (748, 40, 474, 1280), (59, 16, 1341, 384), (1358, 40, 783, 128), (5449, 3, 129, 384), (3747, 40, 1156, 128),
          (4763, 5, 2601, 128), (4815, 40, 1288, 640), (2995, 40, 391, 2304), (5247, 40, 150, 256),
-         (852, 40, 398, 512), (40, 32, 4096, 1024), (700, 32, 4096, 1024)]
+         (852, 40, 398, 512), (40, 32, 4096, 1024), (700, 32, 4096, 1024), (1020, 16, 916, 1152),
+         (6000, 30, 1300, 2304), (2500, 6, 2601, 2304)]
 
 
 @pytest.mark.parametrize("rows,E,N,K", TILES)
@@ -306,6 +307,17 @@ def test_grouped_bf16_odd_steps(K):
     sizes = [3, 0, 40, 17]
     off = sizes_to_offsets(sizes)
     a, w, _, _, av, wv = exact_operands(rng, sum(sizes), len(sizes), 72, K, False)
+    out = ops.moe_grouped_gemm(*put(a, w, torch.from_numpy(off)))
+    np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(O.grouped_product(av, wv, off)))
+
+
+@pytest.mark.parametrize("K", [64, 192, 448])
+def test_grouped_bf16_large_tiles_odd_steps(K):
+    """One, three and seven stages of the largest tile; last blocks of every width class."""
+    rng = np.random.default_rng(K)
+    sizes = [2048 + 65, 1024 + 129, 0, 1, 768 + 64, 512 + 128]
+    off = sizes_to_offsets(sizes)
+    a, w, _, _, av, wv = exact_operands(rng, sum(sizes), len(sizes), 2601, K, False)
     out = ops.moe_grouped_gemm(*put(a, w, torch.from_numpy(off)))
     np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(O.grouped_product(av, wv, off)))
 
