@@ -187,13 +187,17 @@ inline int64_t block_slots(const RowsGemmArgs& g, int bm) {
 }
 
 // Whether the weights pass once and are too many to stay in the 256 MB Infinity
-// Cache for the next call: one row block for each group, on average, and 128
-// MiB of weights or more (one_pass loads, load_piece).  Dense products, us
-// without / with them: 16 x 2112 x 7168 (15 MB) 5.6 / 7.4, 8 x 20000 x 7168
-// (143 MB) 28.3 / 25.7; 32 fp8 groups of 4096 x 2048 (268 MB) 38.0 / 34.4.
+// Cache for the next call: one row block (for groups, whose sizes are known on
+// the device only, half a one on average) and 128 MiB of weights or more
+// (one_pass loads, load_piece).  us without / with them: dense 16 x 2112 x 7168
+// (15 MB) 5.6 / 7.4, 8 x 20000 x 7168 (143 MB) 28.3 / 25.7; 32 fp8 groups of
+// 4096 x 2048 (268 MB) 38.0 / 34.4; 256 fp8 groups of 512 x 4096 in 64-row
+// blocks, half full 133.4 / 125.9; 128 bf16 groups of 4096 x 1536 in 256-row
+// blocks, as many rows as fill one each 526 / 555.
 inline bool one_pass(const RowsGemmArgs& g, int bm, bool fp8) {
     const int64_t groups = g.offsets ? std::min(g.E, g.rows) : 1;
-    return g.rows <= bm * groups && groups * g.N * g.K * (fp8 ? 1 : 2) >= int64_t(128) << 20;
+    const int64_t rows = g.offsets ? 2 * int64_t(g.rows) : g.rows;
+    return rows <= bm * groups && groups * g.N * g.K * (fp8 ? 1 : 2) >= int64_t(128) << 20;
 }
 
 }  // namespace

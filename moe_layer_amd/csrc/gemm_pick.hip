@@ -1,7 +1,7 @@
 // The tile a dense or grouped product runs in.
 //
 // Both forms (gemm_split.hip, gemm_tile.hip) are bound by the bytes a CU gets
-// from L2 into its LDS, 58-86 GB/s by tile, for most sizes: a workgroup of
+// from L2 into its LDS, 59-84 GB/s by tile, for most sizes: a workgroup of
 // BW x BT outputs fetches (BW + BT) 128-byte rows per K step, so large tiles
 // move fewer bytes and small ones fill the 256 CUs.  The time of a tile shape
 // is modelled as
@@ -10,9 +10,9 @@
 // least the bytes that have to come from HBM; the fastest shape is taken.  The
 // constants are a least-squares fit over 61 dense shapes from 1 x 512 x 512 to
 // 8192 x 2112 x 7168, each timed in every tile (those of 256 weight rows where
-// there are more than 128 token rows; residual 7-14 %).  Over those and 27
-// grouped ones the pick is 1.4 % slower than the best tile in the geometric
-// mean, 18 % at worst.
+// there are more than 128 token rows; residual 7-14 %).  Over those and 45
+// grouped ones the pick is 1.9 % slower than the best tile in the geometric
+// mean, 24 % at worst (2000 rows in 32 groups of 2048 x 2048).
 #include <algorithm>
 #include <cmath>
 
