@@ -11,7 +11,10 @@
 //
 // A thread makes 8 columns from 16 bytes of gate and 16 of up; a 128-column
 // quantisation group is 16 neighbouring lanes.  HBM-bound: 4 bytes read per
-// output, 1 + 4/128 (or 2) written.
+// output, 1 + 4/128 (or 2) written; 20011 x 2048 to fp8 44.5 us, 4.64 TB/s (a
+// 1 GiB copy 5.15 TB/s).  Two or four vectors a thread, or loads and stores
+// past the caches' replacement, were no faster.  16 x 2048 2.8 us, of which an
+// empty kernel takes 2.2.
 #include "dense.h"
 
 namespace moe {

@@ -2,7 +2,8 @@
 // allocates the outputs that were not given and calls the C ABI.  These calls
 // stand between two small kernels of a decode step, where ctypes and checks in
 // Python cost more than the kernels (RMSNorm of 64 x 4096 with its residual:
-// 9.2 us a call, 4.3 us of it the ctypes call and the launch).
+// 9.2 us a call that way, 4.3 us of it the ctypes call and the launch; 4.0 us
+// here, about 3 us of it the launch).
 //
 // The library's entry points come in as addresses (bind), so this module works
 // on whichever build of the library the package loaded.  A wrong argument is

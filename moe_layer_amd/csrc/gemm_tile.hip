@@ -9,6 +9,18 @@
 // before.  LDS rows are 128 bytes with chunk c of row r at position
 // c ^ (r & 7), so the 8 lanes that read 8 rows at one chunk hit all banks.
 //
+// What bounds it: at 8192 x 4096 x 7168 fp8 (203 us, 2.37 PFLOP/s; the
+// library's per-tensor product 154 us) the matrix cores are busy for 55 % of the
+// cycles at 2.0 GHz.  Without the folds it took 196 of 207 us, without the loads
+// 164, without both 150: the LDS, which per stage takes in 64 KB and hands out
+// 192 KB to eight waves, is what loads and fragment reads compete for, and four
+// waves of 128 x 128 outputs, which would read a third less, leave no room for
+// the folds (256 fp32 sums a lane besides the vector registers).  Large groups
+// (32768 x 4096 x 1536 bf16 in 128: 520 us, 0.8 PFLOP/s) are bound by the bytes
+// that leave the Infinity Cache and HBM, 2.2 GB read of 1.7 GB operands and 0.27
+// written at 5.1 TB/s, with 4-5 us a tile in which a workgroup stores its
+// outputs and computes nothing.
+//
 // fp8: a stage's products p are one 16x16x128 MFMA per 16 x 16 tile, folded
 // with acc += (a_scale w_scale) p; the scales of 8 stages at a time sit in a
 // two-slot LDS table that is filled along with the ring.
@@ -19,7 +31,8 @@ namespace moe {
 namespace {
 
 // Weight tiles that an XCD's workgroups of one time share with some row blocks
-// (8192 x 4096 x 7168 in 256 x 256 tiles: 2 / 4 / 8 / 16 tiles 231 / 227 / 224 / 229 us).
+// (256 x 256 tiles, 2 / 4 / 8 / 16: 8192 x 4096 x 7168 210 / 208 / 207 / 210 us,
+// 32768 x 4096 x 1536 in 128 bf16 groups 542 / 530 / 530 / 542 us).
 constexpr int kBand = 4;
 
 // Bytes of LDS: the ring and the scale table's two slots

@@ -1,8 +1,10 @@
 """Python binding of libmoe_mi355x.so (include/moe.h).
 
-Argument marshalling only: every step of the layer runs in the library's HIP
-kernels.  torch supplies device memory and the current stream.  If the
-library is missing the first call raises; there is no fallback.
+Argument marshalling only: every step of the layer and every operator around
+it runs in the library's HIP kernels.  torch supplies device memory and the
+current stream.  If the library (or, for the operators around the layer, the
+native binding beside it) is missing the first call raises; there is no
+fallback.
 """
 from __future__ import annotations
 
