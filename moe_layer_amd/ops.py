@@ -432,6 +432,7 @@ def _call(name: str, first: torch.Tensor, *args):
     """A native entry on the current stream of ``first``'s device, with that
     device current."""
     f = getattr(_native or _binding(), name)
+    assert isinstance(first, torch.Tensor), f"moe_{name}: the first operand must be a tensor"
     i = first.get_device()
     if i < 0:                        # not on a GPU: the checks refuse it before anything is launched
         r = f(first, *args, 0)

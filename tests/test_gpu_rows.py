@@ -15,6 +15,8 @@ Comparison rules, fixed before the first run
                                             one per block, up to 16 partial sums joined, and
       fp8: 2^-13 128 sum_b s_b max_k |p_k|  terms below 2^-14 of the largest in their group are dropped; twice that
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -242,6 +244,7 @@ GROUPED = [  # group sizes, rows before the first and behind the last group, N, 
     ([2, 1] * 40 + [0] * 20, 0, 1, 96, 512), ([300, 0, 7], 0, 0, 512, 256), ([0, 511, 1], 0, 9, 384, 640),
     ([1] * 130, 0, 0, 256, 2048), ([40, 60, 3, 0, 128, 256, 255, 70], 5, 6, 320, 256),
     ([128] * 6, 0, 0, 1000, 384), ([600, 500], 0, 0, 1536, 512),
+    ([0] * 700 + [3, 1] * 150 + [0] * 23 + [90], 0, 0, 40, 128),   # the most groups there can be
 ]
 
 
@@ -320,6 +323,23 @@ def test_grouped_bf16_large_tiles_odd_steps(K):
     a, w, _, _, av, wv = exact_operands(rng, sum(sizes), len(sizes), 2601, K, False)
     out = ops.moe_grouped_gemm(*put(a, w, torch.from_numpy(off)))
     np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(O.grouped_product(av, wv, off)))
+
+
+@pytest.mark.parametrize("rows,N,K,fp8", [(3, 40, 2 ** 20, True), (300, 260, 2 ** 16, True), (20, 40, 2 ** 18, False),
+                                          (520, 300, 2 ** 15, False)])
+def test_long_sums(rows, N, K, fp8):
+    """K up to the limit, one group (fp8: the dense product).  bf16 sums take
+    one addition per 32 products, so K / 32 stands in place of K / 128."""
+    rng = np.random.default_rng(K + rows)
+    a, w, sa, sw, av, wv = random_operands(rng, rows, 1, N, K, fp8)
+    ad, wd, sad, swd = put(a, w, sa, sw)
+    if fp8:
+        out = ops.moe_gemm_fp8(ad, sad, wd[0], swd[0])
+    else:
+        out = ops.moe_grouped_gemm(ad, wd, torch.tensor([0, rows], dtype=torch.int32, device=dev()))
+    ref = av @ wv[0].T
+    tol = tolerance(av, wv[0], ref, fp8) + 2.0 ** -24 * (K / 32 - K / 128) * (np.abs(av) @ np.abs(wv[0]).T)
+    assert (np.abs(bf16_to_f64(out) - ref) <= tol).all()
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -556,6 +576,37 @@ def test_two_streams_at_once():
             with torch.cuda.stream(s):
                 chain(st)
     torch.cuda.synchronize()
+    for st, w in zip(states, want):
+        assert same_bits(st["out"], w)
+
+
+def test_two_threads_at_once():
+    """Chains from two threads, each on a stream of its own (the calls run
+    without the interpreter's lock)."""
+    states = [chain_state(s, T=64) for s in (7, 8)]
+    want = []
+    for st in states:
+        chain(st)
+        want.append(st["out"].clone())
+        st["out"].zero_()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(st, s):
+        try:
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    chain(st)
+        except Exception as e:   # noqa: BLE001 - reported by the test
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(st, torch.cuda.Stream())) for st in states]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
     for st, w in zip(states, want):
         assert same_bits(st["out"], w)
 

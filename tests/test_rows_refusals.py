@@ -123,6 +123,9 @@ def test_binding_checks():
             lambda: ops.moe_grouped_gemm(bf(2, 64), u8(3, 8, 64), torch.zeros(4, dtype=torch.int32)),
             lambda: ops.moe_grouped_gemm(u8(2, 128), u8(3, 8, 128), torch.zeros(4, dtype=torch.int32)),
             lambda: ops.moe_grouped_gemm(bf(2, 64), bf(3, 8, 64), torch.zeros(4, dtype=torch.int32), f32(2, 1)),
+            lambda: ops.moe_rmsnorm(None, bf(256)),
+            lambda: ops.moe_gemm_fp8([[1.0]], f32(2, 2), u8(8, 256), f32(1, 2)),
+            lambda: ops.moe_gemm_fp8(u8(2, 256), None, u8(8, 256), f32(1, 2)),
             # right but for the device
             lambda: ops.moe_rmsnorm(bf(2, 256), bf(256)),
             lambda: ops.moe_silu_mul(bf(2, 256), quant="fp8"),
