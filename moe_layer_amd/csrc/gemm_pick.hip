@@ -1,7 +1,7 @@
 // The tile a dense or grouped product runs in.
 //
 // Both forms (gemm_split.hip, gemm_tile.hip) are bound by the bytes a CU gets
-// from L2 into its LDS, 59-84 GB/s by tile, for most sizes: a workgroup of
+// from L2 into its LDS, 50-80 GB/s by tile, for most sizes: a workgroup of
 // BW x BT outputs fetches (BW + BT) 128-byte rows per K step, so large tiles
 // move fewer bytes and small ones fill the 256 CUs.  The time of a tile shape
 // is modelled as
@@ -34,7 +34,7 @@ constexpr Tile kTiles[] = {
     {true, 2, 32, 32, 0.95f, 1.49f, 0.1069f},    {true, 3, 64, 32, 0.83f, 1.91f, 0.1562f},
     {true, 4, 64, 48, 0.68f, 2.53f, 0.1813f},    {true, 5, 64, 64, 0.59f, 2.97f, 0.2185f},
     {true, 6, 64, 80, 0.49f, 3.54f, 0.2398f},    {true, 7, 128, 48, 0.68f, 3.77f, 0.2805f},
-    {false, 0, 64, 16, 2.53f, 0.34f, 0.1219f},   {false, 1, 128, 64, 2.66f, 0.79f, 0.4171f},
+    {false, 0, 64, 32, 2.57f, 0.29f, 0.1760f},   {false, 1, 128, 64, 2.66f, 0.79f, 0.4171f},
     {false, 2, 128, 128, 0.20f, 3.07f, 0.4869f}, {false, 3, 256, 128, 0.48f, 4.37f, 0.8250f},
     {false, 4, 256, 256, -1.06f, 7.37f, 1.3169f},
 };
@@ -54,7 +54,7 @@ double time_us(const Tile& t, const RowsGemmArgs& g, bool fp8) {
     const double bytes = (double(groups) * g.N + g.rows) * g.K * es + 2.0 * g.rows * g.N;
     const double hbm = bytes / kHbmBytesPerUs;
     // long streams overlap with the rest in part only
-    return hbm < 20 ? us : std::max(us, hbm) + 0.3 * std::min(us, hbm);
+    return hbm < 20 ? us : std::max(us, hbm) + (t.split ? 0.3 : 0.2) * std::min(us, hbm);
 }
 
 }  // namespace

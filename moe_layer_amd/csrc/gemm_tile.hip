@@ -316,7 +316,8 @@ hipError_t launch_tile(const RowsGemmArgs& g, hipStream_t s) {
 template <bool FP8>
 hipError_t launch(const RowsGemmArgs& g, int shape, hipStream_t s) {
     switch (shape) {
-        case 0: return launch_tile<FP8, 64, 16, 4, 1, 4>(g, s);
+        // (64 x 16: 300 fp8 rows in 32 groups of 512 x 4096 14.0 -> 12.9 us, 3000 in 256 of 2048 x 2048 200 -> 185)
+        case 0: return launch_tile<FP8, 64, 32, 2, 2, 4>(g, s);
         case 1: return launch_tile<FP8, 128, 64, 4, 1, 3>(g, s);
         case 2: return launch_tile<FP8, 128, 128, 2, 4, 4>(g, s);
         case 3: return launch_tile<FP8, 256, 128, 4, 2, 3>(g, s);
