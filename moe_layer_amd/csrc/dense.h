@@ -102,6 +102,7 @@ struct NormArgs {
     void* scales;
     int rows, cols;
     float eps;
+    double inv_cols;   // 1 / cols
 };
 int norm_max_cols();
 hipError_t launch_norm(const NormArgs& a, int quant, hipStream_t s);

@@ -13,13 +13,46 @@
 // (16 bytes); a 128-column quantisation group is 16 neighbouring lanes.
 // HBM-bound: 2 bytes read (4 with a residual), 2 written for each of r' and y,
 // 1 + 4/128 for the codes and scales.  8192 x 7168 with all of them 95.5 us,
-// 5.55 TB/s (a 1 GiB copy 5.15 TB/s), 1537 x 4096 to MXFP8 7.4 us; 1 x 7168
+// 5.55 TB/s (a 1 GiB copy 5.15 TB/s), 1537 x 4096 to MXFP8 6.8 us; 1 x 7168
 // 3.4 us, of which an empty kernel takes 2.2.
 #include "dense.h"
 
 namespace moe {
 
 namespace {
+
+// A wave's sum, the same bits in every lane: lane permutations inside the
+// vector unit (through LDS, as shuffles go, a sum's six steps wait for it)
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(b)), CTRL, 0xf, 0xf, false));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(b >> 32)), CTRL, 0xf, 0xf, false));
+    return v + __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v = dpp_add<0xb1>(v);                                  // quad_perm [1,0,3,2]
+    v = dpp_add<0x4e>(v);                                  // quad_perm [2,3,0,1]
+    v = dpp_add<0x141>(v);                                 // row_half_mirror
+    v = dpp_add<0x140>(v);                                 // row_mirror
+    auto half = [](double x, auto swap) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        const auto lo = swap(uint32_t(b)), hi = swap(uint32_t(b >> 32));
+        return __builtin_bit_cast(double, uint64_t(hi[0]) << 32 | lo[0]) +
+               __builtin_bit_cast(double, uint64_t(hi[1]) << 32 | lo[1]);
+    };
+    v = half(v, [](uint32_t w) { return __builtin_amdgcn_permlane16_swap(w, w, false, false); });
+    return half(v, [](uint32_t w) { return __builtin_amdgcn_permlane32_swap(w, w, false, false); });
+}
+
+// 1 / sqrt(x) to about 2^-51: the hardware's estimate (good to 2^-14 or better)
+// and three Newton steps, each doubling its bits
+__device__ __forceinline__ double rsqrt64(double x) {
+    double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) y = __fma_rn(y * 0.5, __fma_rn(-x * y, y, 1.0), y);
+    return y;
+}
 
 template <int NT, int CH, int kQuant>
 __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
@@ -53,8 +86,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) sum = __fma_rn(double(v[c][q]), double(v[c][q]), sum);
     }
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) sum += __shfl_xor(sum, m);
+    sum = wave_sum(sum);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = sum;
         __syncthreads();
@@ -62,7 +94,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < NT / 64; ++i) sum += s_part[i];
     }
-    const double inv = 1.0 / sqrt(sum / a.cols + double(a.eps));
+    const double inv = rsqrt64(__fma_rn(sum, a.inv_cols, double(a.eps)));
 
 #pragma unroll
     for (int c = 0; c < CH; ++c) {

@@ -102,6 +102,7 @@ MOE_API int moe_rmsnorm(const void* x, const void* residual, const void* weight,
     a.rows = rows;
     a.cols = cols;
     a.eps = eps;
+    a.inv_cols = 1.0 / cols;
     return hip_status(launch_norm(a, quant_kind(group), stream));
 }
 
