@@ -441,6 +441,29 @@ def test_beyond_32_bits():
     assert not out[:4].any()
 
 
+def test_silu_mul_beyond_one_launch():
+    """More than 2^31 pieces of 8 outputs, which take a second launch: rows on
+    both sides of its border."""
+    d = dev()
+    rows, cols, last = 2 ** 21 + 3, 8192, 8
+    tail = rng_bf16(torch.Generator().manual_seed(31), last, 2 * cols)
+    h = torch.empty(rows, 2 * cols, dtype=torch.bfloat16, device=d)
+    h[-last:] = tail.to(d)
+    _, codes, scales = ops.moe_silu_mul(h, quant="fp8")
+    y = torch.from_numpy(O.silu_mul(bf16_to_f64(tail)).astype(np.float32)).bfloat16().to(d)
+    check_codes("fp8", y, codes[-last:], scales[-last:])
+
+
+@pytest.mark.parametrize("cols", [8, 24, 40, 104, 1000, 2816, 65544])
+def test_silu_mul_row_of_every_piece(cols):
+    """Every 8-column piece reads its own row: gate 1, up the row's number."""
+    rows = 300
+    h = torch.ones(rows, 2 * cols, dtype=torch.bfloat16)
+    h[:, cols:] = torch.arange(rows, dtype=torch.float32).bfloat16()[:, None] % 256
+    y = ops.moe_silu_mul(h.to(dev()))[0]
+    np.testing.assert_array_equal(bf16_to_f64(y), O.silu_mul(bf16_to_f64(h)))
+
+
 # ------------------------------------------------- together, as a user would ---
 
 def test_shared_expert_chain():
