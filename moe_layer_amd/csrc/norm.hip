@@ -12,9 +12,9 @@
 // outputs may replace the inputs).  A thread holds CH chunks of 8 columns
 // (16 bytes); a 128-column quantisation group is 16 neighbouring lanes.
 // HBM-bound: 2 bytes read (4 with a residual), 2 written for each of r' and y,
-// 1 + 4/128 for the codes and scales.  8192 x 7168 with all of them 95.5 us,
-// 5.55 TB/s (a 1 GiB copy 5.15 TB/s), 1537 x 4096 to MXFP8 6.8 us; 1 x 7168
-// 3.4 us, of which an empty kernel takes 2.2.
+// 1 + 4/128 for the codes and scales.  8192 x 7168 with all of them 94.5 us,
+// 5.6 TB/s (a 1 GiB copy 5.15 TB/s), 1537 x 4096 to MXFP8 6.8 us; 1 x 7168
+// 2.7 us, of which an empty kernel takes 2.2.
 #include "dense.h"
 
 namespace moe {
