@@ -475,9 +475,8 @@ MOE_API int moe_silu_mul(const void* h, int32_t rows, int32_t cols, float clamp_
  * (the block-fp8 scheme of P2 section 1.1 without experts):
  *   out[m, n] = bf16(sum_b a_scale[m, b] w_scale[n / 128, b] p(m, n, b)),
  *   p(m, n, b) = sum of a[m, k] w[n, k] over the 128 k of block b.
- * p runs on the fp8 matrix cores, whose dot product drops terms below about
- * 2^-14 of the largest in its group (~1e-4 of a block's sum of magnitudes, a
- * fraction of the output's bf16 rounding); everything else is fp32.
+ * The codes are converted to bf16 exactly; p, its scaling and the sum over the
+ * blocks are fp32.
  *
  *   a        device, E4M3FN [M, K]
  *   a_scale  device, fp32 [M, K / 128] (any finite values)

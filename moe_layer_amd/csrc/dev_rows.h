@@ -37,10 +37,10 @@ __device__ __forceinline__ void wait_stages(int ahead) {
 }
 
 // 16 bytes per lane global -> LDS (lane i's at to + 16 i).  NTW: weights that
-// one row block alone reads go past the caches' replacement (decode-sized
-// groups, 82 of 128 experts of 4096 x 1536 bf16: 143 -> 127 us, 7.2 TB/s;
-// weights that several row blocks read must not: 256-row blocks of the same
-// experts 611 -> 720 us).
+// one row block alone reads go past the caches' replacement (131 rows on 73 of
+// 128 experts of 4096 x 1536 bf16, 0.92 GB: 159 -> 141 us, 6.5 TB/s; weights
+// that several row blocks read must not: 256-row blocks of the same experts,
+// 32768 rows 518 -> 545 us).
 template <bool NTW>
 __device__ __forceinline__ void load_piece(const uint8_t* from, lds_t* to, bool weights) {
     if (NTW && weights)
@@ -161,18 +161,33 @@ __device__ __forceinline__ void store_tile(const RowsGemmArgs& g, const lds_t* t
     else store_rows<BW, BT, THREADS, NT, 1, uint16_t>(g, tile, row0, row1, n0);
 }
 
+// One operand of a 16-row subtile for a 128-byte step of K, from this lane's two
+// 16-byte chunks of its row: bf16 as it is, e4m3 codes as the bf16 values they
+// stand for (exact: 4 significant bits).  The fp8 matrix instructions take the
+// codes themselves and twice as many a cycle, but drop the bits of a product
+// below about 2^-14 of the largest of eight (256 - 256 + 126 times 2^-6 gives 0),
+// and these outputs decide roundings, a gated multiply's codes among them; bf16
+// products are summed in fp32.  Which K a lane's chunks hold does not matter as
+// long as both operands agree.
 template <bool FP8>
-__device__ __forceinline__ f32x4 mma_step(i32x4 a0, i32x4 a1, i32x4 b0, i32x4 b1, f32x4 c) {
-    if constexpr (FP8) {
-        const i32x8 av = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
-        const i32x8 bv = {b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 0, 0, 0, 0, 0, 0);
-    } else {
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a0), __builtin_bit_cast(bf16x8, b0),
-                                                    c, 0, 0, 0);
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a1),
-                                                       __builtin_bit_cast(bf16x8, b1), c, 0, 0, 0);
+struct Operand {
+    static constexpr int kParts = FP8 ? 4 : 2;
+    bf16x8 part[kParts];
+    __device__ __forceinline__ Operand() {}
+    __device__ __forceinline__ Operand(i32x4 c0, i32x4 c1) {
+        if constexpr (FP8) {
+            part[0] = e4m3x8_to_bf16(c0[0], c0[1], 1.0f);
+            part[1] = e4m3x8_to_bf16(c0[2], c0[3], 1.0f);
+            part[2] = e4m3x8_to_bf16(c1[0], c1[1], 1.0f);
+            part[3] = e4m3x8_to_bf16(c1[2], c1[3], 1.0f);
+        } else {
+            part[0] = __builtin_bit_cast(bf16x8, c0);
+            part[1] = __builtin_bit_cast(bf16x8, c1);
+        }
     }
+};
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 // A grid of at least n workgroups, a multiple of 8 of them (xcd_item)
@@ -190,10 +205,10 @@ inline int64_t block_slots(const RowsGemmArgs& g, int bm) {
 // Cache for the next call: one row block (for groups, whose sizes are known on
 // the device only, half a one on average) and 128 MiB of weights or more
 // (one_pass loads, load_piece).  us without / with them: dense 16 x 2112 x 7168
-// (15 MB) 5.6 / 7.4, 8 x 20000 x 7168 (143 MB) 28.3 / 25.7; 32 fp8 groups of
-// 4096 x 2048 (268 MB) 38.0 / 34.4; 256 fp8 groups of 512 x 4096 in 64-row
-// blocks, half full 133.4 / 125.9; 128 bf16 groups of 4096 x 1536 in 256-row
-// blocks, as many rows as fill one each 526 / 555.
+// (15 MB) 6.3 / 7.2, 8 x 20000 x 7168 (143 MB) 31.0 / 27.6; 131 fp8 rows in 32
+// groups of 4096 x 2048 (268 MB) 49.4 / 44.1; 8192 in 256 groups of 512 x 4096,
+// half-full 64-row blocks 142 / 136; 32768 bf16 rows in 128 groups of 4096 x 1536,
+// as many as fill a 256-row block each 518 / 545.
 inline bool one_pass(const RowsGemmArgs& g, int bm, bool fp8) {
     const int64_t groups = g.offsets ? std::min(g.E, g.rows) : 1;
     const int64_t rows = g.offsets ? 2 * int64_t(g.rows) : g.rows;

@@ -16,7 +16,7 @@
 // row pieces at 25-33 TB/s.
 //
 // Bound by the weights' bytes and the loads' latency at few rows (1 x 4096 x
-// 7168 fp8, 29 MB: 6.5 us, 4.5 TB/s; 64 x 7168 x 2048, 16 MB: 5.6 us), beyond
+// 7168 fp8, 29 MB: 7.1 us, 4.1 TB/s; 64 x 7168 x 2048, 16 MB: 6.2 us), beyond
 // by the bytes a CU gets into its LDS (gemm_pick.hip).
 #include "dev_rows.h"
 
@@ -115,18 +115,28 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
         wait_lgkm0();                                            // the slot is in registers: it takes step i + D
         __builtin_amdgcn_sched_barrier(0);
         if (i + D < mine) issue(i + D);
+        using Op = Operand<FP8>;
+        Op bv[SB];
 #pragma unroll
-        for (int m = 0; m < SA; ++m)
+        for (int t = 0; t < SB; ++t) bv[t] = Op(b0[t], b1[t]);
 #pragma unroll
-            for (int t = 0; t < SB; ++t) {
-                if constexpr (FP8) {
-                    const f32x4 p = mma_step<true>(a0[m], a1[m], b0[t], b1[t], f32x4{0, 0, 0, 0});
+        for (int m = 0; m < SA; ++m) {
+            const Op av(a0[m], a1[m]);
+            f32x4 p[SB];                                         // fp8: the step's own sums, to be scaled
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[m][t][q] = __builtin_fmaf(sc[t], p[q], acc[m][t][q]);
-                } else {
-                    acc[m][t] = mma_step<false>(a0[m], a1[m], b0[t], b1[t], acc[m][t]);
+            for (int k = 0; k < Op::kParts; ++k)
+#pragma unroll
+                for (int t = 0; t < SB; ++t) {
+                    if constexpr (FP8) p[t] = mma(av.part[k], bv[t].part[k], k == 0 ? f32x4{0, 0, 0, 0} : p[t]);
+                    else acc[m][t] = mma(av.part[k], bv[t].part[k], acc[m][t]);
                 }
+            if constexpr (FP8) {
+#pragma unroll
+                for (int t = 0; t < SB; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[m][t][q] = __builtin_fmaf(sc[t], p[t][q], acc[m][t][q]);
             }
+        }
     }
     __syncthreads();                                             // the rings are idle: the sums take their place
     f32x4* part = reinterpret_cast<f32x4*>(lds);
@@ -186,10 +196,14 @@ hipError_t launch(const RowsGemmArgs& g, int shape, hipStream_t s) {
         case 3: return launch_split<FP8, 64, 32, 8, 1>(g, s);
         case 4: return launch_split<FP8, 64, 48, 8, 1>(g, s);
         case 5: return launch_split<FP8, 64, 64, 8, 1>(g, s);
-        case 6: return launch_split<FP8, 64, 80, 8, 1>(g, s);
-        case 7: return launch_split<FP8, 128, 48, 6, 1>(g, s);
-        default: return hipErrorInvalidValue;
+        default: break;
     }
+    // of converted e4m3 operands these would not fit the registers
+    if constexpr (!FP8) {
+        if (shape == 6) return launch_split<false, 64, 80, 8, 1>(g, s);
+        if (shape == 7) return launch_split<false, 128, 48, 6, 1>(g, s);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace

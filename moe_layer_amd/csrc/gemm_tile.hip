@@ -9,21 +9,23 @@
 // before.  LDS rows are 128 bytes with chunk c of row r at position
 // c ^ (r & 7), so the 8 lanes that read 8 rows at one chunk hit all banks.
 //
-// What bounds it: at 8192 x 4096 x 7168 fp8 (203 us, 2.37 PFLOP/s; the
-// library's per-tensor product 154 us) the matrix cores are busy for 55 % of the
-// cycles at 2.0 GHz.  Without the folds it took 196 of 207 us, without the loads
-// 164, without both 150: the LDS, which per stage takes in 64 KB and hands out
-// 192 KB to eight waves, is what loads and fragment reads compete for, and four
-// waves of 128 x 128 outputs, which would read a third less, leave no room for
-// the folds (256 fp32 sums a lane besides the vector registers).  Large groups
-// (32768 x 4096 x 1536 bf16 in 128: 520 us, 0.8 PFLOP/s) are bound by the bytes
-// that leave the Infinity Cache and HBM, 2.2 GB read of 1.7 GB operands and 0.27
-// written at 5.1 TB/s, with 4-5 us a tile in which a workgroup stores its
-// outputs and computes nothing.
+// fp8: the codes are converted to bf16 on their way from LDS to the matrix cores
+// (Operand); a stage's products p, four MFMAs per 16 x 16 tile, are folded with
+// acc += (a_scale w_scale) p.  The scales of 8 stages at a time sit in a two-slot
+// LDS table that is filled along with the ring.
 //
-// fp8: a stage's products p are one 16x16x128 MFMA per 16 x 16 tile, folded
-// with acc += (a_scale w_scale) p; the scales of 8 stages at a time sit in a
-// two-slot LDS table that is filled along with the ring.
+// What bounds it: at 8192 x 4096 x 7168 fp8 (410 us, 1.17 PFLOP/s; a library
+// product of bf16 operands of that size 363 us, this file's bf16 form 373) the
+// bf16 matrix cores are busy for 48 % of the cycles at 2.04 GHz and the vector
+// unit, two conversions and a fold a matrix instruction, for most of the rest:
+// without the conversions it took 350 of 422 us, without the folds 386, without
+// the loads 383.  Tiles of 256 x 256, which convert a quarter less, spill (620 us).
+// Reading a stage's first operands in the stage before, 32 x 32 subtiles and loads
+// spread between the products together gave 0-5 % and were not kept.  Large
+// groups (32768 x 4096 x 1536 bf16 in 128: 515 us, 0.8 PFLOP/s) are bound by the
+// bytes that leave the Infinity Cache and HBM, 2.2 GB read of 1.7 GB operands and
+// 0.27 written at 4.8 TB/s, with 4-5 us a tile in which a workgroup stores its
+// outputs and computes nothing.
 #include "dev_rows.h"
 
 namespace moe {
@@ -31,8 +33,8 @@ namespace moe {
 namespace {
 
 // Weight tiles that an XCD's workgroups of one time share with some row blocks
-// (256 x 256 tiles, 2 / 4 / 8 / 16: 8192 x 4096 x 7168 210 / 208 / 207 / 210 us,
-// 32768 x 4096 x 1536 in 128 bf16 groups 542 / 530 / 530 / 542 us).
+// (256 x 256 tiles, 2 / 4 / 8 / 16: 32768 x 4096 x 1536 in 128 bf16 groups
+// 542 / 530 / 530 / 542 us).
 constexpr int kBand = 4;
 
 // Bytes of LDS: the ring and the scale table's two slots
@@ -53,8 +55,7 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     // A ring of two, bf16: every wave has the tokens in registers by the first
     // subtile row and half of its weight rows half-way through the stage, so a
     // second barrier there lets three quarters of the stage after next start
-    // (32768 x 4096 x 1536, 128 groups 589 -> 575 us).  fp8 stages hold as much
-    // arithmetic behind more registers and do not gain (8192 x 4096 x 7168 208 / 213 us).
+    // (32768 x 4096 x 1536, 128 groups 589 -> 575 us).
     constexpr bool kEarly = !FP8 && S == 2;
     constexpr int kHalf0 = NL - BW / 16 / W;                 // its loads of half 0
     static_assert(!kEarly || 2 * 8 * W == BW / WW, "halves of a wave's weight rows");
@@ -145,16 +146,12 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
 #pragma unroll
         for (int t = 0; t < SB; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
 
-    auto fold = [](f32x4& to, float scale, const f32x4& p) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) to[q] = __builtin_fmaf(scale, p[q], to[q]);
-    };
-    f32x4 prev[SB];
-    float last_sc[SB];
+    f32x4 prev[SB];                                          // fp8: the last subtile row's sums over a stage
+    float sc[SB];                                            // and their scales
 #pragma unroll
     for (int t = 0; t < SB; ++t) {
         prev[t] = f32x4{0, 0, 0, 0};
-        last_sc[t] = 0.0f;
+        sc[t] = 0.0f;
     }
 
     if constexpr (FP8) {
@@ -171,39 +168,33 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
         issue_at_start(s);
         if (kEarly && s + S < steps) issue_half_way(s);
     }
+    using Op = Operand<FP8>;
+    // a bf16 stage
     auto stage = [&](int s, auto half_way) {
         wait_stage(s);
         barrier();
-        // fp8: behind the first reads (1024 x 4096 x 4096 24.2 -> 23.2 us); the
-        // bf16 stages, shorter in K, need their loads as early as can be (grouped
-        // 32768 x 4096 x 1536 600 against 616 us)
-        if (!FP8) issue_at_start(s);
+        // the stages, short in K, need their loads as early as can be (grouped 32768
+        // x 4096 x 1536 600 against 616 us behind the first reads)
+        issue_at_start(s);
         const lds_t* from = ring + (s % S) * kSlot;
         // The first product needs one subtile of each operand: those are read
         // first.  Subtile row i is multiplied while row i + 1 is read, behind the
-        // row's first product (in front of it the compiler waits for them as
-        // well), and row i - 1 (for i = 0 the last of the stage before) is folded.
+        // row's first product (in front of it the compiler waits for them as well).
         i32x4 a0 = *reinterpret_cast<lds_v4*>(from + arow + c0), a1 = *reinterpret_cast<lds_v4*>(from + arow + c1);
         i32x4 b0[SB], b1[SB];
-        float sc[SB], sb[SB], sw = 0.0f;
 #pragma unroll
         for (int t = 0; t < SB; ++t) {
             b0[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c0);
             b1[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c1);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (FP8) {
-            issue_at_start(s);
-            __builtin_amdgcn_sched_barrier(0);
-        }
 #pragma unroll
         for (int i = 0; i < SA; ++i) {
             i32x4 n0, n1;
 #pragma unroll
             for (int t = 0; t < SB; ++t) {
-                f32x4 p;
-                if constexpr (FP8) p = mma_step<true>(a0, a1, b0[t], b1[t], f32x4{0, 0, 0, 0});
-                else acc[i][t] = mma_step<false>(a0, a1, b0[t], b1[t], acc[i][t]);
+                const Op av(a0, a1), bv(b0[t], b1[t]);
+                acc[i][t] = mma(av.part[1], bv.part[1], mma(av.part[0], bv.part[0], acc[i][t]));
                 __builtin_amdgcn_sched_barrier(0);
                 if (t == 0 && i + 1 < SA) {
                     n0 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c0);
@@ -213,44 +204,85 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
                     issue_half_way(s);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if constexpr (FP8) {
-                    if (t == 0 && i == 0) {
-                        const lds_t* row = tab + ((s >> 3) & 1) * kTab + (s & 7) * 4;
-                        sw = *reinterpret_cast<lds_f*>(row + (BT + wm * (BW / WW) / 128) * 32);
-#pragma unroll
-                        for (int u = 0; u < SB; ++u)
-                            sb[u] = *reinterpret_cast<lds_f*>(row + (wt * (BT / WT) + 16 * u + lr) * 32);
-                    }
-                    fold(acc[(i + SA - 1) % SA][t], i == 0 ? last_sc[t] : sc[t], prev[t]);
-                    prev[t] = p;
-                    if (t == SB - 1 && i == 0) {
-#pragma unroll
-                        for (int u = 0; u < SB; ++u) sc[u] = __fmul_rn(sb[u], sw);
-                    }
-                }
                 __builtin_amdgcn_sched_barrier(0);
             }
             a0 = n0;
             a1 = n1;
         }
-#pragma unroll
-        for (int t = 0; t < SB; ++t) last_sc[t] = sc[t];
     };
-    // a branch in the middle of a stage would spill (fp8): the last two stages,
-    // which start no third, are their own loop
+    // An fp8 stage: subtile row i is multiplied while row i + 1 is read and
+    // converted and row i - 1 (for i = 0 the last of the stage before) is folded.
+    auto stage8 = [&](int s) {
+        wait_stage(s);
+        barrier();
+        const lds_t* from = ring + (s % S) * kSlot;
+        i32x4 a0 = *reinterpret_cast<lds_v4*>(from + arow + c0), a1 = *reinterpret_cast<lds_v4*>(from + arow + c1);
+        i32x4 b0[SB], b1[SB];
+#pragma unroll
+        for (int t = 0; t < SB; ++t) {
+            b0[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c0);
+            b1[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c1);
+        }
+        const lds_t* row = tab + ((s >> 3) & 1) * kTab + (s & 7) * 4;
+        const float sw = *reinterpret_cast<lds_f*>(row + (BT + wm * (BW / WW) / 128) * 32);
+        float sb[SB];
+#pragma unroll
+        for (int t = 0; t < SB; ++t) sb[t] = *reinterpret_cast<lds_f*>(row + (wt * (BT / WT) + 16 * t + lr) * 32);
+        __builtin_amdgcn_sched_barrier(0);
+        issue_at_start(s);                                   // behind the first reads
+        __builtin_amdgcn_sched_barrier(0);
+        Op av(a0, a1), bv[SB];
+#pragma unroll
+        for (int t = 0; t < SB; ++t) bv[t] = Op(b0[t], b1[t]);
+#pragma unroll
+        for (int i = 0; i < SA; ++i) {
+            Op next;
+            f32x4 p[SB];
+            if (i + 1 < SA) {
+                a0 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c0);
+                a1 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c1);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int t = 0; t < SB; ++t) {
+                    p[t] = mma(av.part[k], bv[t].part[k], k == 0 ? f32x4{0, 0, 0, 0} : p[t]);
+                    f32x4& to = acc[(i + SA - 1) % SA][t];
+                    to[k] = __builtin_fmaf(sc[t], prev[t][k], to[k]);
+                }
+                if (k >= 2 && i + 1 < SA) {                  // the next row's reads have had two parts' time
+                    const i32x4 c = k == 2 ? a0 : a1;
+                    next.part[2 * k - 4] = e4m3x8_to_bf16(c[0], c[1], 1.0f);
+                    next.part[2 * k - 3] = e4m3x8_to_bf16(c[2], c[3], 1.0f);
+                }
+                if (i > 0) __builtin_amdgcn_sched_barrier(0);
+            }
+            av = next;
+#pragma unroll
+            for (int t = 0; t < SB; ++t) {
+                prev[t] = p[t];
+                if (i == 0) sc[t] = __fmul_rn(sb[t], sw);
+            }
+        }
+    };
     const int mine = idle ? 0 : steps;
     int s = 0;
-    for (; kEarly && s + S < mine; ++s) stage(s, std::bool_constant<kEarly>());
-    for (; s < mine; ++s) stage(s, std::false_type());
     if constexpr (FP8) {
+        for (; s < mine; ++s) stage8(s);
 #pragma unroll
-        for (int t = 0; t < SB; ++t) fold(acc[SA - 1][t], last_sc[t], prev[t]);
+        for (int t = 0; t < SB; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[SA - 1][t][q] = __builtin_fmaf(sc[t], prev[t][q], acc[SA - 1][t][q]);
+    } else {
+        // the last two stages, which start no third, are their own loop
+        for (; kEarly && s + S < mine; ++s) stage(s, std::bool_constant<kEarly>());
+        for (; s < mine; ++s) stage(s, std::false_type());
     }
     // The ring is idle: each wave's outputs pass through 16 rows of its own, as
     // it needs no other wave.  The stores of 256 weight rows, long streams for
     // the most part, are past the caches' replacement: 32768 x 4096 x 1536 in 128
-    // groups 574 -> 550 us, and 635 -> 623 us with moe_silu_mul reading the
-    // result; 8192 x 4096 x 7168 213 -> 207 us, 228 -> 227 us with the reader.
+    // bf16 groups 574 -> 550 us, and 635 -> 623 us with moe_silu_mul reading the
+    // result.
     __syncthreads();
     constexpr int kCols = BW / WW;
     lds_t* const rows16 = ring + wv * (16 * kOutRow<kCols>);
@@ -270,8 +302,7 @@ template <bool FP8, int BW, int BT, int WW, int WT, int S, bool NTW>
 __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g, int ntiles, int band) {
     // The last block of a group, of half the rows or fewer: the room of the
     // missing ones goes into a third slot and all waves share the rest (20000
-    // rows in 64 bf16 groups of 2000 x 1024 120 -> 115 us, fp8 32768 x 4096 x
-    // 1536 in 128 351 -> 339 us).
+    // rows in 64 bf16 groups of 2000 x 1024 120 -> 115 us).
     constexpr bool kPart64 = BW == 256, kPart128 = BW == 256 && BT == 256;
     constexpr int kLds = std::max({tile_lds<FP8, BW, BT, S>(), kPart64 ? tile_lds<FP8, BW, 64, 3>() : 0,
                                    kPart128 ? tile_lds<FP8, BW, 128, 3>() : 0});
@@ -316,14 +347,16 @@ hipError_t launch_tile(const RowsGemmArgs& g, hipStream_t s) {
 template <bool FP8>
 hipError_t launch(const RowsGemmArgs& g, int shape, hipStream_t s) {
     switch (shape) {
-        // (64 x 16: 300 fp8 rows in 32 groups of 512 x 4096 14.0 -> 12.9 us, 3000 in 256 of 2048 x 2048 200 -> 185)
         case 0: return launch_tile<FP8, 64, 32, 2, 2, 4>(g, s);
         case 1: return launch_tile<FP8, 128, 64, 4, 1, 3>(g, s);
         case 2: return launch_tile<FP8, 128, 128, 2, 4, 4>(g, s);
         case 3: return launch_tile<FP8, 256, 128, 4, 2, 3>(g, s);
-        case 4: return launch_tile<FP8, 256, 256, 2, 4, 2>(g, s);
-        default: return hipErrorInvalidValue;
+        default: break;
     }
+    if constexpr (!FP8) {                                    // of converted e4m3 operands: out of registers
+        if (shape == 4) return launch_tile<false, 256, 256, 2, 4, 2>(g, s);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace

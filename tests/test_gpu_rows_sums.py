@@ -1,0 +1,64 @@
+"""The sums of the dense and grouped products are 32-bit sums whatever the
+operands' type.
+
+Operands whose products are 2^8 or 2^-6: every 128-block of K holds two columns
+of magnitude 16 on both sides, whose products cancel, and small values of
+magnitude 2^-3 or 0 else.  A block's partial sums are at most 2 2^14 + 126 units
+of 2^-6 and the cancelled blocks' at most 126, times scales of 1 to 4 in units
+of the smallest: exact fp32 values in every order for K <= 2^16, so outputs are
+compared bit for bit.  A dot product that keeps fewer bits below the largest of
+its terms loses the small ones.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from moe_layer_amd import ops
+
+from gpu_util import bf16_to_f64, dev
+from test_gpu_rows import put, sizes_to_offsets
+
+pytestmark = pytest.mark.gpu
+
+
+def wide_operands(rng, rows, E, N, K, fp8):
+    a = (rng.integers(-1, 2, (rows, K)) / 8).astype(np.float32)
+    w = (rng.integers(-1, 2, (E, N, K)) / 8).astype(np.float32)
+    sign = rng.choice([-16.0, 16.0], rows).astype(np.float32)
+    for b in range(0, K, 128):
+        plus, minus = b + rng.choice(min(128, K - b), 2, replace=False)
+        a[:, plus] = a[:, minus] = sign
+        w[:, :, plus], w[:, :, minus] = 16.0, -16.0
+    at, wt = torch.from_numpy(a), torch.from_numpy(w)
+    if not fp8:
+        return at.bfloat16(), wt.bfloat16(), None, None, a.astype(np.float64), w.astype(np.float64)
+    nb = -(-N // 128)
+    sa = rng.choice([0.5, 1.0], (rows, K // 128)).astype(np.float32)
+    sw = rng.choice([1.0, 2.0], (E, nb, K // 128)).astype(np.float32)
+    ac, wc = (t.to(torch.float8_e4m3fn).view(torch.uint8) for t in (at, wt))
+    return (ac, wc, torch.from_numpy(sa), torch.from_numpy(sw), O.act_values(ac.numpy(), sa),
+            O.block_values(wc.numpy(), sw))
+
+
+# from one row to the largest tiles
+@pytest.mark.parametrize("M,N,K", [(1, 40, 128), (1, 4096, 2048), (9, 300, 512), (40, 1000, 2048), (64, 7168, 512),
+                                   (129, 255, 384), (300, 520, 2304), (520, 2000, 640), (770, 4741, 128),
+                                   (1500, 2001, 1152), (2300, 4100, 512)])
+def test_gemm_fp8(M, N, K):
+    rng = np.random.default_rng(M + N + K)
+    a, w, sa, sw, av, wv = wide_operands(rng, M, 1, N, K, True)
+    out = ops.moe_gemm_fp8(*put(a, sa, w[0], sw[0]))
+    np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(av @ wv[0].T))
+
+
+@pytest.mark.parametrize("sizes,N,K", [([5, 0, 1, 18], 130, 256), ([1] * 90, 256, 1024), ([64, 1, 0, 65, 129], 257, 384),
+                                       ([300, 0, 7, 511], 640, 256), ([600, 500, 90], 1536, 512),
+                                       ([2048 + 65, 1024 + 129, 0, 1, 768 + 64], 2601, 256)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_grouped_gemm(sizes, N, K, fp8):
+    rng = np.random.default_rng(sum(sizes) + N + K)
+    a, w, sa, sw, av, wv = wide_operands(rng, sum(sizes), len(sizes), N, K, fp8)
+    off = sizes_to_offsets(sizes)
+    out = ops.moe_grouped_gemm(*put(a, w, torch.from_numpy(off), sa, sw))
+    np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(O.grouped_product(av, wv, off)))
