@@ -464,7 +464,9 @@ MOE_API int moe_rmsnorm(const void* x, const void* residual, const void* weight,
  *   y       device, bf16 [rows, cols]; NULL allowed when quant makes codes (output)
  *   codes, scales  as for moe_rmsnorm (output)
  * No output may overlap h or another output.  clamp_limit >= 0 (0: none).  A
- * NaN or an infinity makes its quantisation group's results unspecified.
+ * NaN of gate or up is one of y and of its code, also behind the clamp; the
+ * other codes and the scale of a quantisation group with a NaN or an infinity
+ * are unspecified.
  * Requires cols % 8 == 0 (FP8_E4M3: % 128, MXFP8: % 32) and cols <= 2^20.
  */
 MOE_API int moe_silu_mul(const void* h, int32_t rows, int32_t cols, float clamp_limit, int32_t quant, void* y,

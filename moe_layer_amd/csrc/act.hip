@@ -80,10 +80,12 @@ __global__ __launch_bounds__(kThreads) void silu_mul_kernel(ActArgs a) {
         u[2 * q + 1] = bf16_hi(uw[q]);
     }
     if constexpr (kClamp) {
+        // comparisons that a NaN fails: it stays (the middle of three alone would take
+        // it for the lowest; NaN-keeping minima 39.4 us at 20011 x 2048, these 37.7)
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            g[q] = __builtin_amdgcn_fmed3f(g[q], -__builtin_inff(), a.limit);
-            u[q] = __builtin_amdgcn_fmed3f(u[q], -a.limit, a.limit);
+            g[q] = g[q] > a.limit ? a.limit : g[q];
+            u[q] = u[q] == u[q] ? __builtin_amdgcn_fmed3f(u[q], -a.limit, a.limit) : u[q];
         }
     }
     float below = 0.0f;                              // not known as a constant, which would undo the choice of fmed3
