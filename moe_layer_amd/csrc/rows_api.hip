@@ -27,12 +27,17 @@ bool overlap(const Span& a, const Span& b) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
     return a0 < b0 + uintptr_t(b.bytes) && b0 < a0 + uintptr_t(a.bytes);
 }
-// any output over an input or another output; an output of `in_place` kind may be an input itself
+// any output over an input or another output; each of the first `in_place` outputs
+// may be one of the first `in_place` inputs itself
 bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins, int in_place) {
     int i = 0;
     for (const Span& o : outs) {
-        for (const Span& n : ins)
-            if (overlap(o, n) && !(i < in_place && o.p == n.p && o.bytes == n.bytes)) return true;
+        int k = 0;
+        for (const Span& n : ins) {
+            const bool itself = i < in_place && k < in_place && o.p == n.p && o.bytes == n.bytes;
+            if (overlap(o, n) && !itself) return true;
+            ++k;
+        }
         int j = 0;
         for (const Span& other : outs)
             if (j++ > i && overlap(o, other)) return true;
