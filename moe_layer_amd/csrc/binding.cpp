@@ -33,6 +33,7 @@ GroupedFn g_grouped;
 
 constexpr int kBf16 = 0, kFp8 = 1, kMx = 2;   // MOE_WDTYPE_*
 
+// (an empty text where a Python exception is set already)
 struct Wrong : std::runtime_error {
     using std::runtime_error::runtime_error;
 };
@@ -125,7 +126,9 @@ float real(PyObject* o) {
 // with_y: None (whether y is given or there is no quantisation), or a truth value
 bool wants_y(PyObject* with_y, PyObject* y, int quant) {
     if (with_y == Py_None) return y != Py_None || quant == kBf16;
-    return PyObject_IsTrue(with_y) == 1;
+    const int yes = PyObject_IsTrue(with_y);
+    if (yes < 0) throw Wrong("");   // with the exception that its truth value raised
+    return yes == 1;
 }
 void make_codes(int quant, int64_t rows, int64_t cols, const at::Tensor& like, Out& codes, Out& scales) {
     const bool mx = quant == kMx;
