@@ -432,7 +432,8 @@ def _call(name: str, first: torch.Tensor, *args):
     """A native entry on the current stream of ``first``'s device, with that
     device current."""
     f = getattr(_native or _binding(), name)
-    assert isinstance(first, torch.Tensor), f"moe_{name}: the first operand must be a tensor"
+    if not isinstance(first, torch.Tensor):   # (raised, not asserted: also under python -O, as the native checks)
+        raise AssertionError(f"moe_{name}: the first operand must be a tensor")
     i = first.get_device()
     if i < 0:                        # not on a GPU: the checks refuse it before anything is launched
         r = f(first, *args, 0)
@@ -447,7 +448,8 @@ def _call(name: str, first: torch.Tensor, *args):
 
 
 def _quant(quant) -> int:
-    assert quant in _QUANT, f"quant: {quant!r}, expected None, 'fp8' or 'mxfp8'"
+    if quant not in _QUANT:
+        raise AssertionError(f"quant: {quant!r}, expected None, 'fp8' or 'mxfp8'")
     return _QUANT[quant]
 
 

@@ -1,6 +1,9 @@
 """The contract of the operators around the layer on the host, where it is
 easily lost: every call here is refused before any device work."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -14,3 +17,27 @@ def test_rmsnorm_one_row_is_not_written_over_the_weight(kw):
     """One row is as long as the weight, which is no row that an output may replace."""
     assert norm(rows=1, **kw) == BAD
     assert norm(rows=1, cols=128, quant=0, codes=None, scales=None, **kw) == BAD
+
+
+def test_refusals_do_not_depend_on_assert_statements():
+    """The same exceptions from an interpreter that skips assert statements."""
+    code = """
+import torch
+from moe_layer_amd import ops
+bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+for call in (lambda: ops.moe_rmsnorm(None, bf(256)),
+             lambda: ops.moe_rmsnorm(bf(2, 256), bf(256), quant="fp4"),
+             lambda: ops.moe_silu_mul([1.0]),
+             lambda: ops.moe_gemm_fp8(None, None, None, None),
+             lambda: ops.moe_grouped_gemm(None, None, None),
+             lambda: ops.moe_silu_mul(bf(2, 256), quant=1)):
+    try:
+        call()
+    except AssertionError:
+        continue
+    raise SystemExit("not refused")
+print("all refused")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(ops.__file__)))
+    r = subprocess.run([sys.executable, "-O", "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "all refused" in r.stdout, r.stderr[-2000:]
