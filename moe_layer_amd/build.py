@@ -45,7 +45,11 @@ def _compile(src: str) -> str:
 
 
 def _build_binding():
-    import torch
+    """The binding, or None where torch is not installed."""
+    try:
+        import torch
+    except ImportError:
+        return None
     tdir = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
@@ -58,25 +62,28 @@ def _build_binding():
     if r.returncode != 0:
         raise RuntimeError(f"binding build failed:\n{r.stderr}")
     os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(verbose: bool = True) -> str:
     """Compile every HIP source and link the shared library, and build the
-    binding; returns the library's path."""
+    binding; returns the library's path.  A C or C++ program needs the library
+    only: it is in place also where the binding fails (an error) or torch is not
+    installed (no binding)."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(min(8, len(srcs) + 1)) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, srcs))
-        binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    bound = binding.result()
     if verbose:
-        print(f"built {LIB} from {len(srcs)} sources")
+        print(f"built {LIB} from {len(srcs)} sources" + ("" if bound else "; no torch, so no Python binding"))
     return LIB
 
 
