@@ -410,11 +410,11 @@ def moe_decode_layer(x, w13, w2, topk_ids=None, topk_weights=None, w13_scale=Non
 
 _QUANT = {None: MOE_WDTYPE_BF16, "fp8": MOE_WDTYPE_FP8_E4M3, "mxfp8": MOE_WDTYPE_MXFP8}
 _native = None
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_current_device = _raw_stream = None   # set with the binding; None on a torch without GPU support
 
 
 def _binding():
-    global _native
+    global _native, _current_device, _raw_stream
     if _native is None:
         try:
             from . import _binding as m
@@ -424,6 +424,8 @@ def _binding():
         L = lib()
         m.bind(*(C.cast(f, C.c_void_p).value for f in (L.moe_rmsnorm, L.moe_silu_mul, L.moe_gemm_fp8,
                                                        L.moe_grouped_gemm)))
+        _current_device = getattr(torch._C, "_cuda_getDevice", None)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _native = m
     return _native
 

@@ -41,3 +41,22 @@ print("all refused")
     root = os.path.dirname(os.path.dirname(os.path.abspath(ops.__file__)))
     r = subprocess.run([sys.executable, "-O", "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "all refused" in r.stdout, r.stderr[-2000:]
+
+
+def test_ops_import_on_a_torch_without_gpu_support():
+    """Such a torch has no current GPU or stream to ask for: importing the
+    package's operators, and what needs neither, works."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    delattr(torch._C, name)
+from moe_layer_amd import ops
+print(ops.lib().moe_status_string(0).decode())
+try:
+    ops.moe_silu_mul(torch.zeros(2, 256, dtype=torch.bfloat16))
+except AssertionError as e:
+    print("refused:", e)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(ops.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "refused:" in r.stdout, r.stderr[-2000:]
