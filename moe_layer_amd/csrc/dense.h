@@ -104,7 +104,6 @@ struct NormArgs {
     float eps;
     double inv_cols;   // 1 / cols
 };
-int norm_max_cols();
 hipError_t launch_norm(const NormArgs& a, int quant, hipStream_t s);
 
 hipError_t launch_silu_mul(const uint16_t* h, int rows, int cols, float clamp_limit, int quant, uint16_t* y,

@@ -15,6 +15,8 @@
 // 1 + 4/128 for the codes and scales.  8192 x 7168 with all of them 94.5 us,
 // 5.6 TB/s (a 1 GiB copy 5.15 TB/s), 1537 x 4096 to MXFP8 6.8 us; 1 x 7168
 // 2.7 us, of which an empty kernel takes 2.2.
+#include "moe.h"
+
 #include "dense.h"
 
 namespace moe {
@@ -140,8 +142,6 @@ hipError_t launch(const NormArgs& a, int quant, hipStream_t s) {
 
 }  // namespace
 
-int norm_max_cols() { return 1024 * 8 * 4; }
-
 // Threads and chunks: few chunks a thread without idle waves.  us, 256 / 512
 // threads: 1537 x 4096 7.05 / 7.47, 1024 x 7168 13.0 / 12.4, 8192 x 7168 95.6 /
 // 94.7, 3000 x 5120 26.1 / 25.0; 128 or 1024 threads are slower throughout.
@@ -152,6 +152,7 @@ hipError_t launch_norm(const NormArgs& a, int quant, hipStream_t s) {
     if (nvec <= 512) return launch<256, 2>(a, quant, s);
     if (nvec <= 1024) return launch<512, 2>(a, quant, s);
     if (nvec <= 2048) return launch<512, 4>(a, quant, s);
+    static_assert(MOE_MAX_NORM_COLS <= 1024 * 4 * 8, "a row in one workgroup's registers");
     return launch<1024, 4>(a, quant, s);
 }
 
