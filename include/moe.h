@@ -481,7 +481,10 @@ MOE_API int moe_silu_mul(const void* h, int32_t rows, int32_t cols, float clamp_
  * blocks are fp32.
  *
  *   a        device, E4M3FN [M, K]
- *   a_scale  device, fp32 [M, K / 128] (any finite values)
+ *   a_scale  device, fp32 [M, K / 128], finite; the product of a row's scale and
+ *            a weight block's is formed in fp32 and has to be 0 or of a magnitude
+ *            in [2^-126, 2^128), else that row's outputs of the block's columns
+ *            are unspecified (an infinity times a zero sum is NaN)
  *   w        device, E4M3FN [N, K]
  *   w_scale  device, fp32 [ceil(N / 128), K / 128]
  *   out      device, bf16 [M, N]   (output; must not overlap an input)

@@ -62,3 +62,25 @@ def test_grouped_gemm(sizes, N, K, fp8):
     off = sizes_to_offsets(sizes)
     out = ops.moe_grouped_gemm(*put(a, w, torch.from_numpy(off), sa, sw))
     np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(O.grouped_product(av, wv, off)))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 256), (40, 300, 256), (300, 520, 384), (1500, 2001, 256)])
+@pytest.mark.parametrize("low", [True, False])
+def test_scale_products_at_the_ends_of_the_range(M, N, K, low):
+    """a_scale w_scale = 2^-126 and 2^127, the smallest and largest powers of two
+    that are normal fp32 values, and zero scales.  Sums of values -1, 0, 1 times
+    2^-9 (low: 1), below 2^11 of their unit, are exact."""
+    rng = np.random.default_rng(M + K)
+    unit = 1.0 if low else 2.0 ** -9
+    a, w = (rng.integers(-1, 2, s).astype(np.float32) for s in ((M, K), (N, K)))
+    ac, wc = (torch.from_numpy(v).to(torch.float8_e4m3fn).view(torch.uint8) for v in (a * np.float32(unit), w))
+    sa = np.full((M, K // 128), 2.0 ** (-100 if low else 100), np.float32)
+    sa[M // 2] = 0.0
+    sw = np.full((-(-N // 128), K // 128), 2.0 ** (-26 if low else 27), np.float32)
+    ref = O.act_values(ac.numpy(), sa) @ O.block_values(wc.numpy(), sw).T
+    args = put(ac, torch.from_numpy(sa), wc, torch.from_numpy(sw))
+    np.testing.assert_array_equal(bf16_to_f64(ops.moe_gemm_fp8(*args)), O.round_bf16(ref))
+    off = torch.tensor([0, M // 3, M], dtype=torch.int32, device=dev())
+    two = [args[2].expand(2, -1, -1).contiguous(), args[3].expand(2, -1, -1).contiguous()]
+    out = ops.moe_grouped_gemm(args[0], two[0], off, args[1], two[1])
+    np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(ref))
