@@ -517,6 +517,20 @@ MOE_API int moe_grouped_gemm(const void* a, const float* a_scale, const void* w,
                              const int32_t* offsets, int32_t rows, int32_t E, int32_t N, int32_t K, int32_t wdtype,
                              void* out, hipStream_t stream);
 
+/* Which kernel moe_gemm_fp8 or moe_grouped_gemm takes for these sizes, reported
+ * like moe_plan_info so that a test can check it without timing. */
+typedef struct moe_gemm_plan_info {
+    int32_t split;       /* 1: K split over a workgroup's waves; 0: tiles shared in LDS */
+    int32_t block_cols;  /* outputs of a row per workgroup */
+    int32_t block_rows;  /* rows of a group per workgroup */
+    int32_t one_pass;    /* 1: the weights are loaded past the caches' replacement */
+} moe_gemm_plan_info;
+
+/* moe_gemm_plan — fill *out (host only, no device work): E = 0 for moe_gemm_fp8
+ * with M = rows and wdtype MOE_WDTYPE_FP8_E4M3, E >= 1 for moe_grouped_gemm.
+ * rows >= 1; otherwise the calls' own requirements and statuses. */
+MOE_API int moe_gemm_plan(int32_t rows, int32_t E, int32_t N, int32_t K, int32_t wdtype, moe_gemm_plan_info* out);
+
 #ifdef __cplusplus
 }
 #endif

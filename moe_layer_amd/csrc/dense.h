@@ -120,8 +120,16 @@ struct RowsGemmArgs {
     int rows, E, N, K;
 };
 hipError_t launch_rows_gemm(const RowsGemmArgs& g, bool fp8, hipStream_t s);
-// its two forms, `shape` one of gemm_pick.hip's tiles
-hipError_t launch_rows_split(const RowsGemmArgs& g, bool fp8, int shape, hipStream_t s);
-hipError_t launch_rows_tile(const RowsGemmArgs& g, bool fp8, int shape, hipStream_t s);
+// the kernel that it takes: the form, its tile (gemm_pick.hip) and whether the
+// weights go past the caches' replacement.  Reads sizes only, of offsets whether
+// they are there.
+struct RowsPlan {
+    bool split;
+    int shape, bw, bt;
+    bool one_pass;
+};
+RowsPlan plan_rows_gemm(const RowsGemmArgs& g, bool fp8);
+hipError_t launch_rows_split(const RowsGemmArgs& g, bool fp8, int shape, bool one_pass, hipStream_t s);
+hipError_t launch_rows_tile(const RowsGemmArgs& g, bool fp8, int shape, bool one_pass, hipStream_t s);
 
 }  // namespace moe

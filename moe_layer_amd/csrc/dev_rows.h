@@ -201,20 +201,6 @@ inline int64_t block_slots(const RowsGemmArgs& g, int bm) {
     return std::min<int64_t>(most, g.rows);
 }
 
-// Whether the weights pass once and are too many to stay in the 256 MB Infinity
-// Cache for the next call: one row block (for groups, whose sizes are known on
-// the device only, half a one on average) and 128 MiB of weights or more
-// (one_pass loads, load_piece).  us without / with them: dense 16 x 2112 x 7168
-// (15 MB) 6.3 / 7.2, 8 x 20000 x 7168 (143 MB) 31.0 / 27.6; 131 fp8 rows in 32
-// groups of 4096 x 2048 (268 MB) 49.4 / 44.1; 8192 in 256 groups of 512 x 4096,
-// half-full 64-row blocks 142 / 136; 32768 bf16 rows in 128 groups of 4096 x 1536,
-// as many as fill a 256-row block each 518 / 545.
-inline bool one_pass(const RowsGemmArgs& g, int bm, bool fp8) {
-    const int64_t groups = g.offsets ? std::min(g.E, g.rows) : 1;
-    const int64_t rows = g.offsets ? 2 * int64_t(g.rows) : g.rows;
-    return rows <= bm * groups && groups * g.N * g.K * (fp8 ? 1 : 2) >= int64_t(128) << 20;
-}
-
 }  // namespace
 
 }  // namespace moe

@@ -69,6 +69,20 @@ double time_us(const Tile& t, const RowsGemmArgs& g, bool fp8) {
     return hbm < 20 ? us : std::max(us, hbm) + (t.split ? 0.3 : 0.2) * std::min(us, hbm);
 }
 
+// Whether the weights pass once and are too many to stay in the 256 MB Infinity
+// Cache for the next call: one row block (for groups, whose sizes are known on
+// the device only, half a one on average) and 128 MiB of weights or more
+// (load_piece).  us without / with them: dense 16 x 2112 x 7168
+// (15 MB) 6.3 / 7.2, 8 x 20000 x 7168 (143 MB) 31.0 / 27.6; 131 fp8 rows in 32
+// groups of 4096 x 2048 (268 MB) 49.4 / 44.1; 8192 in 256 groups of 512 x 4096,
+// half-full 64-row blocks 142 / 136; 32768 bf16 rows in 128 groups of 4096 x 1536,
+// as many as fill a 256-row block each 518 / 545.
+bool one_pass(const RowsGemmArgs& g, int bm, bool fp8) {
+    const int64_t groups = g.offsets ? std::min(g.E, g.rows) : 1;
+    const int64_t rows = g.offsets ? 2 * int64_t(g.rows) : g.rows;
+    return rows <= bm * groups && groups * g.N * g.K * (fp8 ? 1 : 2) >= int64_t(128) << 20;
+}
+
 template <int N>
 const Tile& fastest(const Tile (&tiles)[N], const RowsGemmArgs& g, bool fp8) {
     const Tile* best = tiles;
@@ -85,9 +99,14 @@ const Tile& fastest(const Tile (&tiles)[N], const RowsGemmArgs& g, bool fp8) {
 
 }  // namespace
 
-hipError_t launch_rows_gemm(const RowsGemmArgs& g, bool fp8, hipStream_t s) {
+RowsPlan plan_rows_gemm(const RowsGemmArgs& g, bool fp8) {
     const Tile& t = fp8 ? fastest(kTilesFp8, g, true) : fastest(kTilesBf16, g, false);
-    return t.split ? launch_rows_split(g, fp8, t.shape, s) : launch_rows_tile(g, fp8, t.shape, s);
+    return {t.split, t.shape, t.bw, t.bt, one_pass(g, t.bt, fp8)};
+}
+
+hipError_t launch_rows_gemm(const RowsGemmArgs& g, bool fp8, hipStream_t s) {
+    const RowsPlan p = plan_rows_gemm(g, fp8);
+    return p.split ? launch_rows_split(g, fp8, p.shape, p.one_pass, s) : launch_rows_tile(g, fp8, p.shape, p.one_pass, s);
 }
 
 }  // namespace moe

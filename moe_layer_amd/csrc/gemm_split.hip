@@ -179,37 +179,37 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
 }
 
 template <bool FP8, int BW, int BT, int W, int D>
-hipError_t launch_split(const RowsGemmArgs& g, hipStream_t s) {
+hipError_t launch_split(const RowsGemmArgs& g, bool one_pass, hipStream_t s) {
     const int ntiles = (g.N + BW - 1) / BW;
     const int64_t slots = block_slots(g, BT);
-    void (*kern)(RowsGemmArgs, int, int) = one_pass(g, BT, FP8) ? rows_split_kernel<FP8, BW, BT, W, D, true>
-                                                                      : rows_split_kernel<FP8, BW, BT, W, D, false>;
+    void (*kern)(RowsGemmArgs, int, int) =
+        one_pass ? rows_split_kernel<FP8, BW, BT, W, D, true> : rows_split_kernel<FP8, BW, BT, W, D, false>;
     return start(kern, grid_of(slots * ntiles), 64 * W, s, g, ntiles, int(slots));
 }
 
 template <bool FP8>
-hipError_t launch(const RowsGemmArgs& g, int shape, hipStream_t s) {
+hipError_t launch(const RowsGemmArgs& g, int shape, bool one_pass, hipStream_t s) {
     switch (shape) {
-        case 0: return launch_split<FP8, 16, 16, 8, 4>(g, s);
-        case 1: return launch_split<FP8, 32, 16, 8, 3>(g, s);
-        case 2: return launch_split<FP8, 32, 32, 8, 2>(g, s);
-        case 3: return launch_split<FP8, 64, 32, 8, 1>(g, s);
-        case 4: return launch_split<FP8, 64, 48, 8, 1>(g, s);
-        case 5: return launch_split<FP8, 64, 64, 8, 1>(g, s);
+        case 0: return launch_split<FP8, 16, 16, 8, 4>(g, one_pass, s);
+        case 1: return launch_split<FP8, 32, 16, 8, 3>(g, one_pass, s);
+        case 2: return launch_split<FP8, 32, 32, 8, 2>(g, one_pass, s);
+        case 3: return launch_split<FP8, 64, 32, 8, 1>(g, one_pass, s);
+        case 4: return launch_split<FP8, 64, 48, 8, 1>(g, one_pass, s);
+        case 5: return launch_split<FP8, 64, 64, 8, 1>(g, one_pass, s);
         default: break;
     }
     // of converted e4m3 operands these would not fit the registers
     if constexpr (!FP8) {
-        if (shape == 6) return launch_split<false, 64, 80, 8, 1>(g, s);
-        if (shape == 7) return launch_split<false, 128, 48, 6, 1>(g, s);
+        if (shape == 6) return launch_split<false, 64, 80, 8, 1>(g, one_pass, s);
+        if (shape == 7) return launch_split<false, 128, 48, 6, 1>(g, one_pass, s);
     }
     return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_rows_split(const RowsGemmArgs& g, bool fp8, int shape, hipStream_t s) {
-    return fp8 ? launch<true>(g, shape, s) : launch<false>(g, shape, s);
+hipError_t launch_rows_split(const RowsGemmArgs& g, bool fp8, int shape, bool one_pass, hipStream_t s) {
+    return fp8 ? launch<true>(g, shape, one_pass, s) : launch<false>(g, shape, one_pass, s);
 }
 
 }  // namespace moe

@@ -335,34 +335,33 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
 }
 
 template <bool FP8, int BW, int BT, int WW, int WT, int S>
-hipError_t launch_tile(const RowsGemmArgs& g, hipStream_t s) {
+hipError_t launch_tile(const RowsGemmArgs& g, bool one_pass, hipStream_t s) {
     const int ntiles = (g.N + BW - 1) / BW;
     const int64_t slots = block_slots(g, BT);
-    void (*kern)(RowsGemmArgs, int, int) = one_pass(g, BT, FP8)
-                                               ? rows_tile_kernel<FP8, BW, BT, WW, WT, S, true>
-                                               : rows_tile_kernel<FP8, BW, BT, WW, WT, S, false>;
+    void (*kern)(RowsGemmArgs, int, int) =
+        one_pass ? rows_tile_kernel<FP8, BW, BT, WW, WT, S, true> : rows_tile_kernel<FP8, BW, BT, WW, WT, S, false>;
     return start(kern, xcd_grid(slots * ntiles), 64 * WW * WT, s, g, ntiles, std::min(kBand, ntiles));
 }
 
 template <bool FP8>
-hipError_t launch(const RowsGemmArgs& g, int shape, hipStream_t s) {
+hipError_t launch(const RowsGemmArgs& g, int shape, bool one_pass, hipStream_t s) {
     switch (shape) {
-        case 0: return launch_tile<FP8, 64, 32, 2, 2, 4>(g, s);
-        case 1: return launch_tile<FP8, 128, 64, 4, 1, 3>(g, s);
-        case 2: return launch_tile<FP8, 128, 128, 2, 4, 4>(g, s);
-        case 3: return launch_tile<FP8, 256, 128, 4, 2, 3>(g, s);
+        case 0: return launch_tile<FP8, 64, 32, 2, 2, 4>(g, one_pass, s);
+        case 1: return launch_tile<FP8, 128, 64, 4, 1, 3>(g, one_pass, s);
+        case 2: return launch_tile<FP8, 128, 128, 2, 4, 4>(g, one_pass, s);
+        case 3: return launch_tile<FP8, 256, 128, 4, 2, 3>(g, one_pass, s);
         default: break;
     }
     if constexpr (!FP8) {                                    // of converted e4m3 operands: out of registers
-        if (shape == 4) return launch_tile<false, 256, 256, 2, 4, 2>(g, s);
+        if (shape == 4) return launch_tile<false, 256, 256, 2, 4, 2>(g, one_pass, s);
     }
     return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_rows_tile(const RowsGemmArgs& g, bool fp8, int shape, hipStream_t s) {
-    return fp8 ? launch<true>(g, shape, s) : launch<false>(g, shape, s);
+hipError_t launch_rows_tile(const RowsGemmArgs& g, bool fp8, int shape, bool one_pass, hipStream_t s) {
+    return fp8 ? launch<true>(g, shape, one_pass, s) : launch<false>(g, shape, one_pass, s);
 }
 
 }  // namespace moe

@@ -126,6 +126,25 @@ MOE_API int moe_silu_mul(const void* h, int32_t rows, int32_t cols, float clamp_
                                       static_cast<uint16_t*>(y), codes, scales, stream));
 }
 
+MOE_API int moe_gemm_plan(int32_t rows, int32_t E, int32_t N, int32_t K, int32_t wdtype, moe_gemm_plan_info* out) {
+    if (rows < 1 || E < 0 || E > MOE_MAX_EXPERTS || N <= 0 || K <= 0 || !out) return MOE_ERR_INVALID_ARG;
+    if (wdtype == MOE_WDTYPE_MXFP8) return MOE_ERR_UNSUPPORTED;
+    if (wdtype != MOE_WDTYPE_BF16 && wdtype != MOE_WDTYPE_FP8_E4M3) return MOE_ERR_INVALID_ARG;
+    const bool fp8 = wdtype == MOE_WDTYPE_FP8_E4M3;
+    if ((E == 0 && !fp8) || K % (fp8 ? MOE_QUANT_GROUP : 64) != 0 || rows > kMaxRows || N > kMaxRows || K > kMaxCols)
+        return MOE_ERR_UNSUPPORTED;
+    static const int32_t there = 0;   // the plan looks at no offset
+    RowsGemmArgs g{};
+    g.offsets = E > 0 ? &there : nullptr;
+    g.rows = rows;
+    g.E = E > 0 ? E : 1;
+    g.N = N;
+    g.K = K;
+    const RowsPlan p = plan_rows_gemm(g, fp8);
+    *out = moe_gemm_plan_info{p.split, p.bw, p.bt, p.one_pass};
+    return MOE_OK;
+}
+
 MOE_API int moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int32_t M,
                          int32_t N, int32_t K, void* out, hipStream_t stream) {
     if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;

@@ -29,7 +29,8 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route", "moe_align_capacity"
            "moe_align_scratch_bytes", "moe_align_ws",
            "moe_quant_act", "moe_quant_act_mx", "moe_pack_mx_scales", "moe_plan", "moe_forward_workspace", "moe_forward",
            "moe_forward_profiled", "moe_decode_layer", "moe_forward_noalloc",
-           "moe_rmsnorm", "moe_silu_mul", "moe_gemm_fp8", "moe_grouped_gemm")
+           "moe_rmsnorm", "moe_silu_mul", "moe_gemm_fp8", "moe_grouped_gemm",
+           "moe_gemm_plan")
 MOE_NUM_STAGES = 5
 MOE_NOALLOC_MAX_BYTES = 64 << 20
 MOE_SYNC_WORDS, MOE_SYNC_ERROR = 640, 576
@@ -59,6 +60,10 @@ class PlanInfo(C.Structure):
                 ("off_sorted_ids", C.c_int64), ("off_expert_ids", C.c_int64),
                 ("off_num_post_padded", C.c_int64), ("off_xq", C.c_int64), ("off_xs", C.c_int64),
                 ("off_inter", C.c_int64), ("off_inter_scale", C.c_int64), ("off_y", C.c_int64)]
+
+
+class GemmPlanInfo(C.Structure):
+    _fields_ = [("split", C.c_int32), ("block_cols", C.c_int32), ("block_rows", C.c_int32), ("one_pass", C.c_int32)]
 
 
 def lib() -> C.CDLL:
@@ -108,6 +113,8 @@ def lib() -> C.CDLL:
         L.moe_gemm_fp8.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp]
         L.moe_grouped_gemm.restype = C.c_int
         L.moe_grouped_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+        L.moe_gemm_plan.restype = C.c_int
+        L.moe_gemm_plan.argtypes = [i32, i32, i32, i32, i32, C.POINTER(GemmPlanInfo)]
         _lib = L
     return _lib
 
@@ -491,3 +498,11 @@ def moe_grouped_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, a_
     K/128].  Returns bf16 out [rows, N]; rows outside every group keep what
     out held (uninitialised when it is allocated here)."""
     return _call("grouped_gemm", a, w, offsets, a_scale, w_scale, out)
+
+
+def moe_gemm_plan(rows: int, N: int, K: int, E: int = 0, wdtype: int = MOE_WDTYPE_FP8_E4M3) -> dict:
+    """Which kernel moe_gemm_fp8 (E = 0) or moe_grouped_gemm (E experts) takes
+    for these sizes (host only)."""
+    info = GemmPlanInfo()
+    _check("moe_gemm_plan", lib().moe_gemm_plan(rows, E, N, K, wdtype, C.byref(info)))
+    return {name: getattr(info, name) for name, _ in GemmPlanInfo._fields_}
