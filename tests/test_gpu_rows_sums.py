@@ -84,3 +84,35 @@ def test_scale_products_at_the_ends_of_the_range(M, N, K, low):
     two = [args[2].expand(2, -1, -1).contiguous(), args[3].expand(2, -1, -1).contiguous()]
     out = ops.moe_grouped_gemm(args[0], two[0], off, args[1], two[1])
     np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(ref))
+
+
+@pytest.mark.parametrize("rows,E,N,K,fp8", [(3, 0, 40, 2 ** 20, True), (300, 0, 260, 2 ** 16, True), (70, 0, 130, 2 ** 17 + 128, True),
+                                            (40, 3, 70, 2 ** 18, True), (20, 1, 40, 2 ** 18, False),
+                                            (520, 2, 300, 2 ** 15 + 64, False), (9, 2, 33, 2 ** 20, False)])
+def test_long_sums_are_complete(rows, E, N, K, fp8):
+    """One product of magnitude 1 for every 128 of K, at a place that moves
+    through the block, so that a lost step changes every output by 1; most sums,
+    of up to 2^13 random signs, stay below 256, where bf16 shows a difference of 1."""
+    rng = np.random.default_rng(K + rows)
+    groups = max(E, 1)
+    a = np.zeros((rows, K), np.float32)
+    w = rng.choice([-1.0, 1.0], (groups, N, K)).astype(np.float32)
+    steps = -(-K // 128)
+    for r in range(rows):
+        at = 128 * np.arange(steps) + (37 * np.arange(steps) + 11 * r) % 128
+        at[0], at[-1] = 0, K - 1                            # the first and the last of K
+        a[r, at] = rng.choice([-1.0, 1.0], steps)
+    off = sizes_to_offsets(rng.multinomial(rows, [1 / groups] * groups))
+    ref = O.grouped_product(a.astype(np.float64), w.astype(np.float64), off)
+    assert (np.abs(ref) < 256).mean() > 0.9
+    at, wt = torch.from_numpy(a), torch.from_numpy(w)
+    if not fp8:
+        out = ops.moe_grouped_gemm(*put(at.bfloat16(), wt.bfloat16(), torch.from_numpy(off)))
+    else:
+        ac, wc = (t.to(torch.float8_e4m3fn).view(torch.uint8) for t in (at, wt))
+        sa, sw = torch.ones(rows, K // 128), torch.ones(groups, -(-N // 128), K // 128)
+        if E == 0:
+            out = ops.moe_gemm_fp8(*put(ac, sa, wc[0], sw[0]))
+        else:
+            out = ops.moe_grouped_gemm(*put(ac, wc, torch.from_numpy(off), sa, sw))
+    np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(ref))
