@@ -16,7 +16,7 @@ import torch
 import oracle as O
 from moe_layer_amd import ops
 
-from gpu_util import bf16_to_f64, dev
+from gpu_util import bf16_to_f64, dev, log
 from test_gpu_rows import put, sizes_to_offsets
 
 pytestmark = pytest.mark.gpu
@@ -116,3 +116,33 @@ def test_long_sums_are_complete(rows, E, N, K, fp8):
         else:
             out = ops.moe_grouped_gemm(*put(ac, wc, torch.from_numpy(off), sa, sw))
     np.testing.assert_array_equal(bf16_to_f64(out), O.round_bf16(ref))
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_codes_behind_a_product(grouped):
+    """The codes that moe_silu_mul makes of a gate/up product are those of its
+    64-bit sum, but for values next to a rounding border.  A 32-bit sum of 4096
+    random products is off by about 2^-25 sqrt(128) = 3e-7 of itself, so about
+    3e-7 / 2^-8 = 1e-4 of the bf16 gate and up values round the other way, and one
+    in 16 of those moves a 4-bit code: 1e-5 of the codes.  20 times that is
+    allowed (a sum that loses 2^-14 of its largest products flips 2e-3 of them)."""
+    rng = np.random.default_rng(41)
+    rows, E, K, I = 128, 2, 4096, 512
+    a = (rng.standard_normal((rows, K)) * 60).clip(-448, 448).astype(np.float32)
+    w = (rng.standard_normal((E, 2 * I, K)) * 60).clip(-448, 448).astype(np.float32)
+    ac, wc = (torch.from_numpy(v).to(torch.float8_e4m3fn).view(torch.uint8) for v in (a, w))
+    sa = (2.0 ** rng.integers(-9, -6, (rows, K // 128))).astype(np.float32)
+    sw = (1e-4 * (1 + rng.random((E, 2 * I // 128, K // 128)))).astype(np.float32)
+    av, wv = O.act_values(ac.numpy(), sa), O.block_values(wc.numpy(), sw)
+    if grouped:
+        off = np.array([0, 50, rows], np.int32)
+        ref = O.grouped_product(av, wv, off)
+        h = ops.moe_grouped_gemm(*put(ac, wc, torch.from_numpy(off), torch.from_numpy(sa), torch.from_numpy(sw)))
+    else:
+        ref = av @ wv[0].T
+        h = ops.moe_gemm_fp8(*put(ac, torch.from_numpy(sa), wc[0], torch.from_numpy(sw[0])))
+    _, codes, _ = ops.moe_silu_mul(h, quant="fp8")
+    want, _, _ = O.quant_act(O.silu_mul(O.round_bf16(O.fl32(ref))))
+    off_by = int((codes.cpu().numpy() != want).sum())
+    log(f"codes behind a product: {off_by} of {want.size} differ")
+    assert off_by <= 2e-4 * want.size
