@@ -16,8 +16,9 @@
 //
 // What bounds it: at 8192 x 4096 x 7168 fp8 (410 us, 1.17 PFLOP/s; a library
 // product of bf16 operands of that size 363 us, this file's bf16 form 373) the
-// bf16 matrix cores are busy for 48 % of the cycles at 2.04 GHz and the vector
-// unit, two conversions and a fold a matrix instruction, for most of the rest:
+// bf16 matrix cores are busy for 48 % of the cycles (counted in a profiled run)
+// and the vector unit, two conversions and a fold a matrix instruction, for most
+// of the rest:
 // without the conversions it took 350 of 422 us, without the folds 386, without
 // the loads 383.  Tiles of 256 x 256, which convert a quarter less, spill (620 us).
 // Reading a stage's first operands in the stage before, 32 x 32 subtiles and loads
