@@ -54,6 +54,8 @@ extern "C" {
 #define MOE_WDTYPE_FP8_E4M3  1   /* w13/w2 are E4M3FN with 128x128 fp32 block scales */
 #define MOE_WDTYPE_MXFP8     2   /* w13/w2 are E4M3FN with one E8M0 scale per row and
                                     32 consecutive K elements (MXFP8) */
+#define MOE_WDTYPE_INT8      4   /* 8-bit integers with one fp32 scale per row; the
+                                    operators around the layer only */
 
 /* GEMM tile path (moe_forward_args.path) */
 #define MOE_PATH_AUTO        0   /* the planner decides from rows per expert */
@@ -420,6 +422,7 @@ MOE_API int moe_decode_layer(const moe_forward_args* a, const float* router_logi
  * MOE_WDTYPE_MXFP8, MOE_WDTYPE_BF16 for no codes.
  * ------------------------------------------------------------------------ */
 #define MOE_MAX_NORM_COLS 32768
+#define MOE_MAX_INT8_K    32768  /* columns of an int8 row */
 
 /*
  * moe_rmsnorm — residual addition and RMSNorm in front of the layer, with its
@@ -473,6 +476,36 @@ MOE_API int moe_silu_mul(const void* h, int32_t rows, int32_t cols, float clamp_
                          uint8_t* codes, void* scales, hipStream_t stream);
 
 /*
+ * moe_quant_act_int8 — bf16 rows as 8-bit integers with one scale per row, the
+ * activation side of the int8 products:
+ *   m = max(max |x|, fl32(1e-10)),  scale = fl32(m / 127),
+ *   code = RNE(x fl32(127 / m))     (the exact product, rounded once; |code| <= 127)
+ * A row with a NaN or an infinity gets the scale NaN and unspecified codes, so
+ * the outputs that an int8 product makes of it are NaN.
+ *
+ *   x       device, bf16 [rows, cols]
+ *   codes   device, int8 [rows, cols]   (output)
+ *   scales  device, fp32 [rows], 4-byte aligned (output)
+ * No output may overlap x or another output.  Requires cols % 16 == 0 and cols
+ * <= MOE_MAX_INT8_K, else MOE_ERR_UNSUPPORTED.
+ */
+MOE_API int moe_quant_act_int8(const void* x, int32_t rows, int32_t cols, int8_t* codes, float* scales,
+                               hipStream_t stream);
+
+/*
+ * moe_silu_mul_int8 — moe_silu_mul's y, quantised as moe_quant_act_int8 does:
+ * the step between an expert's two int8 products.
+ *
+ *   h       device, bf16 [rows, 2 * cols] (a w13 product's rows)
+ *   codes   device, int8 [rows, cols]   (output)
+ *   scales  device, fp32 [rows], 4-byte aligned (output)
+ * No output may overlap h or another output.  clamp_limit >= 0 (0: none).
+ * Requires cols % 16 == 0 and cols <= MOE_MAX_INT8_K, else MOE_ERR_UNSUPPORTED.
+ */
+MOE_API int moe_silu_mul_int8(const void* h, int32_t rows, int32_t cols, float clamp_limit, int8_t* codes,
+                              float* scales, hipStream_t stream);
+
+/*
  * moe_gemm_fp8 — dense product of quantised rows with block-scaled weights
  * (the block-fp8 scheme of P2 section 1.1 without experts):
  *   out[m, n] = bf16(sum_b a_scale[m, b] w_scale[n / 128, b] p(m, n, b)),
@@ -494,30 +527,47 @@ MOE_API int moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* 
                          int32_t N, int32_t K, void* out, hipStream_t stream);
 
 /*
+ * moe_gemm_int8 — dense product of 8-bit integers with a scale per token and per
+ * output channel:
+ *   out[m, n] = bf16(fl32(fl32(S) a_scale[m]) w_scale[n]),  S = sum_k a[m, k] w[n, k],
+ * S an exact 32-bit integer, fl32 and bf16 to the nearest.
+ *
+ *   a        device, int8 [M, K] (every value, -128 included)
+ *   a_scale  device, fp32 [M]
+ *   w        device, int8 [N, K]
+ *   w_scale  device, fp32 [N]
+ *   out      device, bf16 [M, N]   (output; must not overlap an input)
+ * Requires N >= 1, K % 16 == 0, 16 <= K <= MOE_MAX_INT8_K and M, N <= 2^30.
+ */
+MOE_API int moe_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale, int32_t M,
+                          int32_t N, int32_t K, void* out, hipStream_t stream);
+
+/*
  * moe_grouped_gemm — products of rows that are already sorted by expert, the
  * groups ragged and unpadded (the sorted rows of P2 section 1.1 without the
  * block padding):
  *   out[r, n] = bf16(sum_k a[r, k] w[e, n, k]) for offsets[e] <= r < offsets[e+1]
- * in bf16 (fp32 sums), or in fp8 with moe_gemm_fp8's scales and arithmetic.
- * Rows outside every group (before offsets[0], from offsets[E] on) are neither
- * read nor written; groups may be empty.
+ * in bf16 (fp32 sums), in fp8 with moe_gemm_fp8's scales and arithmetic, or in
+ * 8-bit integers with moe_gemm_int8's.  Rows outside every group (before offsets[0], from offsets[E]
+ * on) are neither read nor written; groups may be empty.
  *
- *   a        device, bf16 or E4M3FN [rows, K]
- *   a_scale  device, fp32 [rows, K / 128] (FP8_E4M3), else NULL
- *   w        device, bf16 or E4M3FN [E, N, K]
- *   w_scale  device, fp32 [E, ceil(N / 128), K / 128] (FP8_E4M3), else NULL
+ *   a        device, bf16, E4M3FN or int8 [rows, K]
+ *   a_scale  device, fp32 [rows, K / 128] (FP8_E4M3) or [rows] (INT8), else NULL
+ *   w        device, bf16, E4M3FN or int8 [E, N, K]
+ *   w_scale  device, fp32 [E, ceil(N / 128), K / 128] (FP8_E4M3) or [E, N] (INT8), else NULL
  *   offsets  device, int32 [E + 1], ascending, in [0, rows] (a table that is
  *            not gives unspecified rows, never an access out of bounds)
  *   out      device, bf16 [rows, N]   (output; must not overlap an input)
- * wdtype is MOE_WDTYPE_BF16 or MOE_WDTYPE_FP8_E4M3 (MXFP8: MOE_ERR_UNSUPPORTED).
- * Requires 1 <= E <= MOE_MAX_EXPERTS, N >= 1, K % 64 == 0 (bf16) or K % 128
- * == 0 (fp8), K <= 2^20, and rows, N <= 2^30.
+ * wdtype is MOE_WDTYPE_BF16, MOE_WDTYPE_FP8_E4M3 or MOE_WDTYPE_INT8 (MXFP8:
+ * MOE_ERR_UNSUPPORTED).
+ * Requires 1 <= E <= MOE_MAX_EXPERTS, N >= 1, K % 64 == 0 (bf16), K % 128 == 0
+ * (fp8) or K % 16 == 0 (int8), K <= 2^20 (int8: MOE_MAX_INT8_K), and rows, N <= 2^30.
  */
 MOE_API int moe_grouped_gemm(const void* a, const float* a_scale, const void* w, const float* w_scale,
                              const int32_t* offsets, int32_t rows, int32_t E, int32_t N, int32_t K, int32_t wdtype,
                              void* out, hipStream_t stream);
 
-/* Which kernel moe_gemm_fp8 or moe_grouped_gemm takes for these sizes, reported
+/* Which kernel moe_gemm_fp8, moe_gemm_int8 or moe_grouped_gemm takes for these sizes, reported
  * like moe_plan_info so that a test can check it without timing. */
 typedef struct moe_gemm_plan_info {
     int32_t split;       /* 1: K split over a workgroup's waves; 0: tiles shared in LDS */
@@ -527,9 +577,91 @@ typedef struct moe_gemm_plan_info {
 } moe_gemm_plan_info;
 
 /* moe_gemm_plan — fill *out (host only, no device work): E = 0 for moe_gemm_fp8
- * with M = rows and wdtype MOE_WDTYPE_FP8_E4M3, E >= 1 for moe_grouped_gemm.
+ * (wdtype MOE_WDTYPE_FP8_E4M3) or moe_gemm_int8 (MOE_WDTYPE_INT8) with M = rows,
+ * E >= 1 for moe_grouped_gemm.
  * rows >= 1; otherwise the calls' own requirements and statuses. */
 MOE_API int moe_gemm_plan(int32_t rows, int32_t E, int32_t N, int32_t K, int32_t wdtype, moe_gemm_plan_info* out);
+
+/*
+ * moe_sort_scratch_bytes — device scratch bytes moe_sort_rows needs for T * topk
+ * slots over E experts: 0 for few slots, whose positions are found in the launch
+ * that moves the rows, else an int32 per expert and block of slots (at most 256
+ * blocks).  Host only; negative status on invalid arguments.
+ */
+MOE_API int64_t moe_sort_scratch_bytes(int32_t T, int32_t topk, int32_t E);
+
+/*
+ * moe_sort_rows — tokens' rows in the order moe_grouped_gemm takes them: sorted
+ * by expert, unpadded, a token's row once for each of its routed slots.  With
+ * flat slots f = t * topk + j, routed where 0 <= topk_ids[f] < E:
+ *   offsets[e] = the number of slots routed to experts below e (offsets[E]: to any),
+ *   inv[f] = offsets[topk_ids[f]] + the number of smaller f routed to the same
+ *            expert; -1 for an unrouted slot,
+ *   rows[inv[f]] = x[t], row_scales[inv[f]] = x_scale[t] or what quantising x[t] makes.
+ * Rows from offsets[E] on, and their scales, are not written.
+ *
+ *   x           device, [T, cols] of xtype: MOE_WDTYPE_BF16; MOE_WDTYPE_FP8_E4M3
+ *               (moe_quant_act's codes); MOE_WDTYPE_INT8 (moe_quant_act_int8's)
+ *   x_scale     device, fp32 [T, cols / 128] (FP8_E4M3), [T] (INT8), else NULL
+ *   topk_ids    device, int32 [T, topk]
+ *   rowtype     xtype, or, where xtype is MOE_WDTYPE_BF16, MOE_WDTYPE_FP8_E4M3
+ *               or MOE_WDTYPE_INT8: x is quantised on the way by moe_quant_act's
+ *               or moe_quant_act_int8's rule
+ *   rows        device, [T * topk, cols] of rowtype                 (output)
+ *   row_scales  device, fp32 [T * topk, cols / 128] or [T * topk]; NULL for bf16
+ *               rows, 4-byte aligned                                (output)
+ *   offsets     device, int32 [E + 1]                               (output)
+ *   inv         device, int32 [T, topk]                             (output)
+ *   scratch     device, >= moe_sort_scratch_bytes(T, topk, E) bytes, 4-byte
+ *               aligned (may be NULL when that is 0); contents on entry do not
+ *               matter; owned by the caller
+ * No output (and no scratch) may overlap an input or another output.  T == 0
+ * sets the offsets to 0.  Requires 1 <= E <= MOE_MAX_EXPERTS, 1 <= topk <=
+ * MOE_MAX_TOPK, T * topk <= 2^30, cols % 8 == 0 for bf16, % 128 for FP8_E4M3,
+ * % 16 for INT8 on either side, cols <= 2^20 (quantised to int8: MOE_MAX_INT8_K).
+ * MOE_ERR_WORKSPACE when the scratch is missing, misaligned or too small.
+ */
+MOE_API int moe_sort_rows(const void* x, const float* x_scale, const int32_t* topk_ids, int32_t T, int32_t topk,
+                          int32_t E, int32_t cols, int32_t xtype, int32_t rowtype, void* rows, float* row_scales,
+                          int32_t* offsets, int32_t* inv, void* scratch, int64_t scratch_bytes, hipStream_t stream);
+
+/*
+ * moe_combine_rows — the experts' rows back at their tokens, weighted:
+ *   out[t] = bf16(sum_j weights[t, j] rows[inv[t, j]])
+ * summed in fp32 in slot order (a fused multiply-add per slot).  Without weights
+ * they are 1: that is the gradient of moe_sort_rows with respect to x, given the
+ * gradient of its (bf16) rows.  Slots whose inv lies outside [0, num_rows) add
+ * nothing, whatever any row holds; a token without a routed slot gets 0.
+ *
+ *   rows     device, bf16 [num_rows, cols]
+ *   inv      device, int32 [T, topk] (moe_sort_rows)
+ *   weights  device, fp32 [T, topk] or NULL
+ *   out      device, bf16 [T, cols]   (output; must not overlap an input)
+ * Requires 1 <= topk <= MOE_MAX_TOPK, cols % 8 == 0, cols <= 2^20, T * topk <= 2^30
+ * and 0 <= num_rows <= 2^30 (rows may be NULL where num_rows is 0).
+ */
+MOE_API int moe_combine_rows(const void* rows, const int32_t* inv, const float* weights, int32_t T, int32_t topk,
+                             int32_t cols, int32_t num_rows, void* out, hipStream_t stream);
+
+/*
+ * moe_combine_rows_bwd — the gradients of moe_combine_rows:
+ *   grad_rows[inv[t, j]] = bf16(weights[t, j] grad_out[t])
+ *   grad_weights[t, j] = sum_h grad_out[t, h] rows[inv[t, j], h]   (fp32)
+ * Slots whose inv lies outside [0, num_rows) have no row and grad_weights 0.
+ * Rows that no slot has are not written; a row that two slots have (moe_sort_rows
+ * makes no such inv) gets the gradient of one of them.
+ *
+ *   grad_out      device, bf16 [T, cols]
+ *   rows          device, bf16 [num_rows, cols]; NULL where grad_weights is NULL
+ *   inv           device, int32 [T, topk]
+ *   weights       device, fp32 [T, topk] or NULL (1)
+ *   grad_rows     device, bf16 [num_rows, cols]   (output)
+ *   grad_weights  device, fp32 [T, topk] or NULL  (output)
+ * No output may overlap an input or another output.  Sizes as for moe_combine_rows.
+ */
+MOE_API int moe_combine_rows_bwd(const void* grad_out, const void* rows, const int32_t* inv, const float* weights,
+                                 int32_t T, int32_t topk, int32_t cols, int32_t num_rows, void* grad_rows,
+                                 float* grad_weights, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -5,8 +5,8 @@
 // the optional clamp of the bf16 gate and up values before it, and codes and
 // scales by moe_quant_act's rule.
 //
-// g is a bf16 value, so bf16(silu(g)) is a function of 16 bits; silu_f32 below
-// gives its correct rounding for every finite g (a test compares all of them
+// g is a bf16 value, so bf16(silu(g)) is a function of 16 bits; silu_f32
+// (dev_silu.h) gives its correct rounding for every finite g (a test compares all of them
 // with 64-bit arithmetic), so the outputs are the definition's bit for bit.
 //
 // A thread makes 8 columns from 16 bytes of gate and 16 of up; a 128-column
@@ -21,33 +21,13 @@
 
 #include <algorithm>
 
-#include "dense.h"
+#include "dev_silu.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-// silu(g) without overflow on either side: z = exp(-|g|) = h^2, h = 2^(c |g|)
-// with c = -log2(e) / 2 in two parts.  c_hi has 16 bits, so its product with a
-// bf16 |g| is exact; 2^(c_lo |g|) is 1 + c_lo ln(2) |g| to 2^-24.  r = 1 / (1 + z)
-// with one Newton step, silu = g r for g >= 0 and g r h h else (z itself would
-// be subnormal where silu is not).  Without the Newton step one of the 65280
-// finite gates (5.9375) rounds to the wrong bf16.
-__device__ __forceinline__ float silu_f32(float g, float below) {
-    constexpr float kHi = -0.721343994140625f;                      // -log2(e) / 2 in 16 bits
-    constexpr float kLo = -2.444247576e-06f;                   // ln(2) times the rest
-    // min(|g|, 1000), where z and silu(-a) have long been 0: the middle of three
-    // is one instruction, a minimum makes its operand canonical first
-    const float a = __builtin_amdgcn_fmed3f(__builtin_fabsf(g), below, 1000.0f);
-    float h = __builtin_amdgcn_exp2f(a * kHi);
-    h = __builtin_fmaf(h, a * kLo, h);
-    const float d = __builtin_fmaf(h, h, 1.0f);
-    float r = __builtin_amdgcn_rcpf(d);
-    r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
-    return g < 0.0f ? -a * r * h * h : g * r;
-}
 
 struct ActArgs {
     const uint16_t* h;      // [rows, 2 cols]
@@ -71,31 +51,7 @@ __global__ __launch_bounds__(kThreads) void silu_mul_kernel(ActArgs a) {
     const uint32_t cols = a.per_row * 8;
     const i32x4 gw = *reinterpret_cast<const i32x4*>(src);
     const i32x4 uw = *reinterpret_cast<const i32x4*>(src + cols);
-    float g[8], u[8];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        g[2 * q] = bf16_lo(gw[q]);
-        g[2 * q + 1] = bf16_hi(gw[q]);
-        u[2 * q] = bf16_lo(uw[q]);
-        u[2 * q + 1] = bf16_hi(uw[q]);
-    }
-    if constexpr (kClamp) {
-        // comparisons that a NaN fails: it stays (the middle of three alone would take
-        // it for the lowest; NaN-keeping minima 39.4 us at 20011 x 2048, these 37.7)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            g[q] = g[q] > a.limit ? a.limit : g[q];
-            u[q] = u[q] == u[q] ? __builtin_amdgcn_fmed3f(u[q], -a.limit, a.limit) : u[q];
-        }
-    }
-    float below = 0.0f;                              // not known as a constant, which would undo the choice of fmed3
-    asm("" : "+v"(below));
-    i32x4 o;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint32_t sl = pack_bf16(silu_f32(g[2 * q], below), silu_f32(g[2 * q + 1], below));
-        o[q] = int(pack_bf16(__fmul_rn(bf16_lo(sl), u[2 * q]), __fmul_rn(bf16_hi(sl), u[2 * q + 1])));
-    }
+    const i32x4 o = silu_mul8<kClamp>(gw, uw, a.limit);
     if (live && a.y) *reinterpret_cast<i32x4*>(a.y + at) = o;
     if constexpr (kQuant != 0) {
         constexpr int kLanes = kQuant == 1 ? 16 : 4;

@@ -110,16 +110,17 @@ hipError_t launch_silu_mul(const uint16_t* h, int rows, int cols, float clamp_li
                            uint8_t* codes, void* scales, hipStream_t s);
 
 // out[r, n] = bf16(sum_k a[r, k] w[e, n, k]) for the rows r of group e
+enum RowsKind { kRowsBf16, kRowsFp8, kRowsInt8 };
 struct RowsGemmArgs {
-    const uint8_t* a;          // [rows, K] bf16 or e4m3
-    const float* a_scale;      // [rows, K / 128] (fp8)
+    const uint8_t* a;          // [rows, K] bf16, e4m3 or int8
+    const float* a_scale;      // [rows, K / 128] (fp8), [rows] (int8)
     const uint8_t* w;          // [E, N, K]
-    const float* w_scale;      // [E, ceil(N / 128), K / 128] (fp8)
+    const float* w_scale;      // [E, ceil(N / 128), K / 128] (fp8), [E, N] (int8)
     const int32_t* offsets;    // [E + 1] device, or null: one group of all rows
     uint16_t* out;             // bf16 [rows, N]
     int rows, E, N, K;
 };
-hipError_t launch_rows_gemm(const RowsGemmArgs& g, bool fp8, hipStream_t s);
+hipError_t launch_rows_gemm(const RowsGemmArgs& g, RowsKind kind, hipStream_t s);
 // the kernel that it takes: the form, its tile (gemm_pick.hip) and whether the
 // weights go past the caches' replacement.  Reads sizes only, of offsets whether
 // they are there.
@@ -128,8 +129,8 @@ struct RowsPlan {
     int shape, bw, bt;
     bool one_pass;
 };
-RowsPlan plan_rows_gemm(const RowsGemmArgs& g, bool fp8);
-hipError_t launch_rows_split(const RowsGemmArgs& g, bool fp8, int shape, bool one_pass, hipStream_t s);
-hipError_t launch_rows_tile(const RowsGemmArgs& g, bool fp8, int shape, bool one_pass, hipStream_t s);
+RowsPlan plan_rows_gemm(const RowsGemmArgs& g, RowsKind kind);
+hipError_t launch_rows_split(const RowsGemmArgs& g, RowsKind kind, int shape, bool one_pass, hipStream_t s);
+hipError_t launch_rows_tile(const RowsGemmArgs& g, RowsKind kind, int shape, bool one_pass, hipStream_t s);
 
 }  // namespace moe

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dense.h"
 
@@ -167,27 +168,47 @@ __device__ __forceinline__ void store_tile(const RowsGemmArgs& g, const lds_t* t
 // codes themselves and twice as many a cycle, but drop the bits of a product
 // below about 2^-14 of the largest of eight (256 - 256 + 126 times 2^-6 gives 0),
 // and these outputs decide roundings, a gated multiply's codes among them; bf16
-// products are summed in fp32.  Which K a lane's chunks hold does not matter as
-// long as both operands agree.
-template <bool FP8>
+// products are summed in fp32.  int8 codes go to the matrix cores as they are and
+// are summed in 32-bit integers, exactly.  Which K a lane's chunks hold does not
+// matter as long as both operands agree.
+template <RowsKind KIND>
 struct Operand {
-    static constexpr int kParts = FP8 ? 4 : 2;
-    bf16x8 part[kParts];
+    static constexpr int kParts = KIND == kRowsFp8 ? 4 : 2;
+    using Part = std::conditional_t<KIND == kRowsInt8, i32x4, bf16x8>;
+    Part part[kParts];
     __device__ __forceinline__ Operand() {}
     __device__ __forceinline__ Operand(i32x4 c0, i32x4 c1) {
-        if constexpr (FP8) {
+        if constexpr (KIND == kRowsFp8) {
             part[0] = e4m3x8_to_bf16(c0[0], c0[1], 1.0f);
             part[1] = e4m3x8_to_bf16(c0[2], c0[3], 1.0f);
             part[2] = e4m3x8_to_bf16(c1[0], c1[1], 1.0f);
             part[3] = e4m3x8_to_bf16(c1[2], c1[3], 1.0f);
         } else {
-            part[0] = __builtin_bit_cast(bf16x8, c0);
-            part[1] = __builtin_bit_cast(bf16x8, c1);
+            part[0] = __builtin_bit_cast(Part, c0);
+            part[1] = __builtin_bit_cast(Part, c1);
         }
     }
 };
 __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ i32x4 mma(i32x4 a, i32x4 b, i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+// a lane's four sums of a 16 x 16 subtile
+template <RowsKind KIND>
+using Sums = std::conditional_t<KIND == kRowsInt8, i32x4, f32x4>;
+
+// int8: rows of K bytes, any multiple of 16, so the last step of 128 may be a part
+// of one.  Lanes whose 16-byte chunk lies behind a row's end fetch zeros there.
+__device__ const __attribute__((aligned(16))) uint8_t kNoChunk[16] = {};
+
+// The outputs of four int8 sums: fl32(fl32(sum) a_scale) w_scale, each rounded
+__device__ __forceinline__ f32x4 scaled(i32x4 sum, float sa, f32x4 sw) {
+    f32x4 v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = __fmul_rn(__fmul_rn(float(sum[q]), sa), sw[q]);
+    return v;
 }
 
 // A grid of at least n workgroups, a multiple of 8 of them (xcd_item)

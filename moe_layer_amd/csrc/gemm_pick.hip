@@ -53,8 +53,8 @@ constexpr Tile kTilesFp8[] = {
 
 constexpr double kHbmBytesPerUs = 5.8e6;   // streaming reads and writes (6 TB/s reads alone)
 
-double time_us(const Tile& t, const RowsGemmArgs& g, bool fp8) {
-    const double es = fp8 ? 1 : 2, steps = g.K * es / 128;
+double time_us(const Tile& t, const RowsGemmArgs& g, RowsKind kind) {
+    const double es = kind == kRowsBf16 ? 2 : 1, steps = std::ceil(g.K * es / 128);
     const int64_t groups = g.offsets ? std::min(g.E, g.rows) : 1;
     // row blocks: of a group's rows, known on the device only, the last one is
     // half full on average
@@ -77,18 +77,18 @@ double time_us(const Tile& t, const RowsGemmArgs& g, bool fp8) {
 // groups of 4096 x 2048 (268 MB) 49.4 / 44.1; 8192 in 256 groups of 512 x 4096,
 // half-full 64-row blocks 142 / 136; 32768 bf16 rows in 128 groups of 4096 x 1536,
 // as many as fill a 256-row block each 518 / 545.
-bool one_pass(const RowsGemmArgs& g, int bm, bool fp8) {
+bool one_pass(const RowsGemmArgs& g, int bm, RowsKind kind) {
     const int64_t groups = g.offsets ? std::min(g.E, g.rows) : 1;
     const int64_t rows = g.offsets ? 2 * int64_t(g.rows) : g.rows;
-    return rows <= bm * groups && groups * g.N * g.K * (fp8 ? 1 : 2) >= int64_t(128) << 20;
+    return rows <= bm * groups && groups * g.N * g.K * (kind == kRowsBf16 ? 2 : 1) >= int64_t(128) << 20;
 }
 
 template <int N>
-const Tile& fastest(const Tile (&tiles)[N], const RowsGemmArgs& g, bool fp8) {
+const Tile& fastest(const Tile (&tiles)[N], const RowsGemmArgs& g, RowsKind kind) {
     const Tile* best = tiles;
-    double least = time_us(tiles[0], g, fp8);
+    double least = time_us(tiles[0], g, kind);
     for (const Tile& t : tiles) {
-        const double us = time_us(t, g, fp8);
+        const double us = time_us(t, g, kind);
         if (us < least) {
             best = &t;
             least = us;
@@ -99,14 +99,14 @@ const Tile& fastest(const Tile (&tiles)[N], const RowsGemmArgs& g, bool fp8) {
 
 }  // namespace
 
-RowsPlan plan_rows_gemm(const RowsGemmArgs& g, bool fp8) {
-    const Tile& t = fp8 ? fastest(kTilesFp8, g, true) : fastest(kTilesBf16, g, false);
-    return {t.split, t.shape, t.bw, t.bt, one_pass(g, t.bt, fp8)};
+RowsPlan plan_rows_gemm(const RowsGemmArgs& g, RowsKind kind) {
+    const Tile& t = kind == kRowsFp8 ? fastest(kTilesFp8, g, kind) : fastest(kTilesBf16, g, kind);
+    return {t.split, t.shape, t.bw, t.bt, one_pass(g, t.bt, kind)};
 }
 
-hipError_t launch_rows_gemm(const RowsGemmArgs& g, bool fp8, hipStream_t s) {
-    const RowsPlan p = plan_rows_gemm(g, fp8);
-    return p.split ? launch_rows_split(g, fp8, p.shape, p.one_pass, s) : launch_rows_tile(g, fp8, p.shape, p.one_pass, s);
+hipError_t launch_rows_gemm(const RowsGemmArgs& g, RowsKind kind, hipStream_t s) {
+    const RowsPlan p = plan_rows_gemm(g, kind);
+    return p.split ? launch_rows_split(g, kind, p.shape, p.one_pass, s) : launch_rows_tile(g, kind, p.shape, p.one_pass, s);
 }
 
 }  // namespace moe

@@ -1,8 +1,8 @@
 // Dense and grouped products of few rows, or of few tiles:
 //   out[r, n] = bf16(sum_k a[r, k] w[e, n, k]),  offsets[e] <= r < offsets[e + 1]
 // (dense: one group of all rows), for bf16 operands or e4m3 ones with an fp32
-// scale per row and 128 K (a) and per 128 x 128 block (w).  gemm_tile.hip has
-// the form for many tiles.
+// scale per row and 128 K (a) and per 128 x 128 block (w), or int8 ones with an
+// fp32 scale per row of a and of w.  gemm_tile.hip has the form for many tiles.
 //
 // The weight rows are the MFMA M side and the token rows the N side, so a lane
 // holds one token and four neighbouring outputs of it.  A workgroup owns BW
@@ -24,9 +24,11 @@ namespace moe {
 
 namespace {
 
-template <bool FP8, int BW, int BT, int W, int D, bool NTW>
+template <RowsKind KIND, int BW, int BT, int W, int D, bool NTW>
 __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int ntiles, int slots) {
     constexpr int SA = BW / 16, SB = BT / 16;
+    constexpr bool FP8 = KIND == kRowsFp8, INT8 = KIND == kRowsInt8;
+    using Acc = Sums<KIND>;
     // the step's scales behind its rows: BT of the tokens, then the weights' one
     constexpr int kScaleLoads = FP8 ? BT / 64 + 1 : 0;
     constexpr int kSlot = (BW + BT) * 128 + 256 * kScaleLoads;
@@ -46,8 +48,8 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lk = lane >> 4;
-    const int64_t kbytes = int64_t(g.K) * (FP8 ? 1 : 2);
-    const int steps = int(kbytes >> 7);
+    const int64_t kbytes = int64_t(g.K) * (KIND == kRowsBf16 ? 2 : 1);
+    const int steps = int((kbytes + 127) >> 7);
     const int n0 = tile * BW;
     lds_t* const ring = (lds_t*)lds + wv * D * kSlot;
 
@@ -62,6 +64,8 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
         const int r = 8 * j + (lane >> 3);
         off[j] = uint32_t(8 * j < BW ? min(r, last_w) : min(r - BW, last_a)) * uint32_t(kbytes) + chunk;
     }
+    const int part = INT8 && (kbytes & 127) ? steps - 1 : -1;    // the step that is a part of one
+    const bool past = int(chunk) >= int(kbytes & 127);
     const float* sp[kScaleLoads + 1];                            // this lane's scale rows
 #pragma unroll
     for (int j = 0; j < kScaleLoads; ++j) {
@@ -79,16 +83,34 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
 #pragma unroll
         for (int j = 0; j < (BW + BT) / 8; ++j) {
             const uint8_t* base = (8 * j < BW ? wbase : abase) + (int64_t(s) << 7);
-            load_piece<NTW>(base + off[j], to + j * 1024, 8 * j < BW);
+            const uint8_t* from = base + off[j];
+            if (INT8 && s == part && past) from = kNoChunk;
+            load_piece<NTW>(from, to + j * 1024, 8 * j < BW);
         }
     };
     const uint32_t c0 = uint32_t(lr * 128) + (uint32_t(lk ^ (lr & 7)) << 4), c1 = c0 ^ 64;
 
-    f32x4 acc[SA][SB];
+    Acc acc[SA][SB];
 #pragma unroll
     for (int i = 0; i < SA; ++i)
 #pragma unroll
-        for (int t = 0; t < SB; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < SB; ++t) acc[i][t] = Acc{0, 0, 0, 0};
+
+    // the subtiles whose sums this wave finishes; int8: their scales, asked for
+    // before everything else
+    constexpr int kMine = (SA * SB + W - 1) / W;
+    float sa[kMine];
+    f32x4 sw4[kMine];
+    if constexpr (INT8) {
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            const int j = min(wv + W * q, SA * SB - 1);
+            sa[q] = g.a_scale[min(row0 + 16 * (j % SB) + lr, row1 - 1)];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                sw4[q][k] = g.w_scale[int64_t(e) * g.N + min(n0 + 16 * (j / SB) + 4 * lk + k, g.N - 1)];
+        }
+    }
 
     const int mine = steps > wv ? (steps - wv + W - 1) / W : 0;  // this wave's steps
     for (int i = 0; i < D && i < mine; ++i) issue(i);
@@ -115,7 +137,7 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
         wait_lgkm0();                                            // the slot is in registers: it takes step i + D
         __builtin_amdgcn_sched_barrier(0);
         if (i + D < mine) issue(i + D);
-        using Op = Operand<FP8>;
+        using Op = Operand<KIND>;
         Op bv[SB];
 #pragma unroll
         for (int t = 0; t < SB; ++t) bv[t] = Op(b0[t], b1[t]);
@@ -139,24 +161,28 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
         }
     }
     __syncthreads();                                             // the rings are idle: the sums take their place
-    f32x4* part = reinterpret_cast<f32x4*>(lds);
+    Acc* sums = reinterpret_cast<Acc*>(lds);
 #pragma unroll
     for (int m = 0; m < SA; ++m)
 #pragma unroll
-        for (int t = 0; t < SB; ++t) part[(wv * SA * SB + m * SB + t) * 64 + lane] = acc[m][t];
+        for (int t = 0; t < SB; ++t) sums[(wv * SA * SB + m * SB + t) * 64 + lane] = acc[m][t];
     __syncthreads();
-    constexpr int kMine = (SA * SB + W - 1) / W;
     f32x4 v[kMine];
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
         const int j = min(wv + W * q, SA * SB - 1);
-        v[q] = part[j * 64 + lane];
+        Acc sum = sums[j * 64 + lane];
 #pragma unroll
         for (int i = 1; i < W; ++i) {
-            const f32x4 o = part[(i * SA * SB + j) * 64 + lane];
+            const Acc o = sums[(i * SA * SB + j) * 64 + lane];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[q][k] = __fadd_rn(v[q][k], o[k]);
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (INT8) sum[k] += o[k];
+                else sum[k] = __fadd_rn(sum[k], o[k]);
+            }
         }
+        if constexpr (INT8) v[q] = scaled(sum, sa[q], sw4[q]);
+        else v[q] = sum;
     }
     if ((g.N & 3) == 0) {                                        // whole 8-byte pieces of a row
 #pragma unroll
@@ -178,38 +204,42 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
     store_tile<BW, BT, 64 * W, false>(g, (lds_t*)lds, row0, row1, n0);
 }
 
-template <bool FP8, int BW, int BT, int W, int D>
+template <RowsKind KIND, int BW, int BT, int W, int D>
 hipError_t launch_split(const RowsGemmArgs& g, bool one_pass, hipStream_t s) {
     const int ntiles = (g.N + BW - 1) / BW;
     const int64_t slots = block_slots(g, BT);
     void (*kern)(RowsGemmArgs, int, int) =
-        one_pass ? rows_split_kernel<FP8, BW, BT, W, D, true> : rows_split_kernel<FP8, BW, BT, W, D, false>;
+        one_pass ? rows_split_kernel<KIND, BW, BT, W, D, true> : rows_split_kernel<KIND, BW, BT, W, D, false>;
     return start(kern, grid_of(slots * ntiles), 64 * W, s, g, ntiles, int(slots));
 }
 
-template <bool FP8>
+template <RowsKind KIND>
 hipError_t launch(const RowsGemmArgs& g, int shape, bool one_pass, hipStream_t s) {
     switch (shape) {
-        case 0: return launch_split<FP8, 16, 16, 8, 4>(g, one_pass, s);
-        case 1: return launch_split<FP8, 32, 16, 8, 3>(g, one_pass, s);
-        case 2: return launch_split<FP8, 32, 32, 8, 2>(g, one_pass, s);
-        case 3: return launch_split<FP8, 64, 32, 8, 1>(g, one_pass, s);
-        case 4: return launch_split<FP8, 64, 48, 8, 1>(g, one_pass, s);
-        case 5: return launch_split<FP8, 64, 64, 8, 1>(g, one_pass, s);
+        case 0: return launch_split<KIND, 16, 16, 8, 4>(g, one_pass, s);
+        case 1: return launch_split<KIND, 32, 16, 8, 3>(g, one_pass, s);
+        case 2: return launch_split<KIND, 32, 32, 8, 2>(g, one_pass, s);
+        case 3: return launch_split<KIND, 64, 32, 8, 1>(g, one_pass, s);
+        case 4: return launch_split<KIND, 64, 48, 8, 1>(g, one_pass, s);
+        case 5: return launch_split<KIND, 64, 64, 8, 1>(g, one_pass, s);
         default: break;
     }
     // of converted e4m3 operands these would not fit the registers
-    if constexpr (!FP8) {
-        if (shape == 6) return launch_split<false, 64, 80, 8, 1>(g, one_pass, s);
-        if (shape == 7) return launch_split<false, 128, 48, 6, 1>(g, one_pass, s);
+    if constexpr (KIND != kRowsFp8) {
+        if (shape == 6) return launch_split<KIND, 64, 80, 8, 1>(g, one_pass, s);
+        if (shape == 7) return launch_split<KIND, 128, 48, 6, 1>(g, one_pass, s);
     }
     return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_rows_split(const RowsGemmArgs& g, bool fp8, int shape, bool one_pass, hipStream_t s) {
-    return fp8 ? launch<true>(g, shape, one_pass, s) : launch<false>(g, shape, one_pass, s);
+hipError_t launch_rows_split(const RowsGemmArgs& g, RowsKind kind, int shape, bool one_pass, hipStream_t s) {
+    switch (kind) {
+        case kRowsBf16: return launch<kRowsBf16>(g, shape, one_pass, s);
+        case kRowsFp8: return launch<kRowsFp8>(g, shape, one_pass, s);
+        default: return launch<kRowsInt8>(g, shape, one_pass, s);
+    }
 }
 
 }  // namespace moe

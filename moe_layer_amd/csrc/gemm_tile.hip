@@ -38,16 +38,19 @@ namespace {
 // 542 / 530 / 530 / 542 us).
 constexpr int kBand = 4;
 
-// Bytes of LDS: the ring and the scale table's two slots
-template <bool FP8, int BW, int BT, int S>
+// Bytes of LDS: the ring and the scale table's two slots (int8: the tile's scales)
+template <RowsKind KIND, int BW, int BT, int S>
 constexpr int tile_lds() {
-    const int rows = FP8 ? (BT + (BW + 127) / 128 + 7) / 8 * 8 : 0;
-    return S * (BW + BT) * 128 + 2 * rows * 32;
+    const int rows = KIND == kRowsFp8 ? (BT + (BW + 127) / 128 + 7) / 8 * 8 : 0;
+    const int scales = KIND == kRowsInt8 ? (BW + BT + 63) / 64 * 256 : 0;
+    return S * (BW + BT) * 128 + 2 * rows * 32 + scales;
 }
 
 // One tile: weight rows n0 .. n0 + BW - 1 against rows row0 .. min(row0 + BT, row1) - 1 of group e
-template <bool FP8, int BW, int BT, int WW, int WT, int S, bool NTW>
+template <RowsKind KIND, int BW, int BT, int WW, int WT, int S, bool NTW>
 __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring, int e, int row0, int row1, int n0) {
+    constexpr bool FP8 = KIND == kRowsFp8, INT8 = KIND == kRowsInt8;
+    using Acc = Sums<KIND>;
     constexpr int W = WW * WT;
     constexpr int SA = BW / WW / 16, SB = BT / WT / 16;      // 16-row subtiles per wave
     constexpr int kPieces = (BW + BT) / 8;                   // 1 KB loads per stage
@@ -71,8 +74,10 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wv % WW, wt = wv / WW;
     const int lr = lane & 15, lk = lane >> 4;
-    const int64_t kbytes = int64_t(g.K) * (FP8 ? 1 : 2);
-    const int steps = int(kbytes >> 7);
+    const int64_t kbytes = int64_t(g.K) * (KIND == kRowsBf16 ? 2 : 1);
+    const int steps = int((kbytes + 127) >> 7);
+    const int part = INT8 && (kbytes & 127) ? steps - 1 : -1;   // the step that is a part of one
+    const bool past = (((lane & 7) ^ (lane >> 3)) << 4) >= int(kbytes & 127);
 
     const uint8_t* wbase = g.w + (int64_t(e) * g.N + n0) * kbytes;
     const uint8_t* abase = g.a + int64_t(row0) * kbytes;
@@ -85,7 +90,9 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     }
     auto load = [&](int st, int j) {
         const uint8_t* base = (j < BW / 8 / W ? wbase : abase) + (int64_t(st) << 7);
-        load_piece<NTW>(base + off[j], ring + (st % S) * kSlot + min(wv + W * j, kPieces - 1) * 1024, j < BW / 8 / W);
+        const uint8_t* from = base + off[j];
+        if (INT8 && st == part && past) from = kNoChunk;
+        load_piece<NTW>(from, ring + (st % S) * kSlot + min(wv + W * j, kPieces - 1) * 1024, j < BW / 8 / W);
     };
     // pieces of half 0: the tokens and the first half of each wave's weight rows; of half 1: the rest
     auto half_of = [](int j) { return j < BW / 8 / W ? j & 1 : 0; };
@@ -141,11 +148,11 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     const uint32_t brow = uint32_t(BW + wt * (BT / WT) + lr) * 128;
     const uint32_t c0 = uint32_t(lk ^ (lr & 7)) << 4, c1 = c0 ^ 64;
 
-    f32x4 acc[SA][SB];
+    Acc acc[SA][SB];
 #pragma unroll
     for (int i = 0; i < SA; ++i)
 #pragma unroll
-        for (int t = 0; t < SB; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < SB; ++t) acc[i][t] = Acc{0, 0, 0, 0};
 
     f32x4 prev[SB];                                          // fp8: the last subtile row's sums over a stage
     float sc[SB];                                            // and their scales
@@ -159,6 +166,15 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
 #pragma unroll
         for (int p = 0; p < kParts; ++p) issue_scales(0, p);
     }
+    if constexpr (INT8) {                                    // the tile's scales, weight rows first: 64 a load
+#pragma unroll
+        for (int p = wv; p < (BW + BT + 63) / 64; p += W) {
+            const int i = 64 * p + lane;
+            const float* src = i < BW ? w_scale + int64_t(e) * g.N + min(n0 + i, g.N - 1)
+                                      : a_scale + min(row0 + i - BW, row1 - 1);
+            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(src), tab + 256 * p, 4, 0, 0);
+        }
+    }
     for (int st = 0; st < S - 1 && st < steps; ++st) issue_stage(st, -1);
     if (kEarly && S - 1 < steps) issue_stage(S - 1, 0);
     // a wave whose tokens or weight rows all lie past the end only loads
@@ -169,8 +185,8 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
         issue_at_start(s);
         if (kEarly && s + S < steps) issue_half_way(s);
     }
-    using Op = Operand<FP8>;
-    // a bf16 stage
+    using Op = Operand<KIND>;
+    // a bf16 or int8 stage
     auto stage = [&](int s, auto half_way) {
         wait_stage(s);
         barrier();
@@ -214,55 +230,57 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     // An fp8 stage: subtile row i is multiplied while row i + 1 is read and
     // converted and row i - 1 (for i = 0 the last of the stage before) is folded.
     auto stage8 = [&](int s) {
-        wait_stage(s);
-        barrier();
-        const lds_t* from = ring + (s % S) * kSlot;
-        i32x4 a0 = *reinterpret_cast<lds_v4*>(from + arow + c0), a1 = *reinterpret_cast<lds_v4*>(from + arow + c1);
-        i32x4 b0[SB], b1[SB];
-#pragma unroll
-        for (int t = 0; t < SB; ++t) {
-            b0[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c0);
-            b1[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c1);
-        }
-        const lds_t* row = tab + ((s >> 3) & 1) * kTab + (s & 7) * 4;
-        const float sw = *reinterpret_cast<lds_f*>(row + (BT + wm * (BW / WW) / 128) * 32);
-        float sb[SB];
-#pragma unroll
-        for (int t = 0; t < SB; ++t) sb[t] = *reinterpret_cast<lds_f*>(row + (wt * (BT / WT) + 16 * t + lr) * 32);
-        __builtin_amdgcn_sched_barrier(0);
-        issue_at_start(s);                                   // behind the first reads
-        __builtin_amdgcn_sched_barrier(0);
-        Op av(a0, a1), bv[SB];
-#pragma unroll
-        for (int t = 0; t < SB; ++t) bv[t] = Op(b0[t], b1[t]);
-#pragma unroll
-        for (int i = 0; i < SA; ++i) {
-            Op next;
-            f32x4 p[SB];
-            if (i + 1 < SA) {
-                a0 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c0);
-                a1 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c1);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                for (int t = 0; t < SB; ++t) {
-                    p[t] = mma(av.part[k], bv[t].part[k], k == 0 ? f32x4{0, 0, 0, 0} : p[t]);
-                    f32x4& to = acc[(i + SA - 1) % SA][t];
-                    to[k] = __builtin_fmaf(sc[t], prev[t][k], to[k]);
-                }
-                if (k >= 2 && i + 1 < SA) {                  // the next row's reads have had two parts' time
-                    const i32x4 c = k == 2 ? a0 : a1;
-                    next.part[2 * k - 4] = e4m3x8_to_bf16(c[0], c[1], 1.0f);
-                    next.part[2 * k - 3] = e4m3x8_to_bf16(c[2], c[3], 1.0f);
-                }
-                if (i > 0) __builtin_amdgcn_sched_barrier(0);
-            }
-            av = next;
+        if constexpr (FP8) {
+            wait_stage(s);
+            barrier();
+            const lds_t* from = ring + (s % S) * kSlot;
+            i32x4 a0 = *reinterpret_cast<lds_v4*>(from + arow + c0), a1 = *reinterpret_cast<lds_v4*>(from + arow + c1);
+            i32x4 b0[SB], b1[SB];
 #pragma unroll
             for (int t = 0; t < SB; ++t) {
-                prev[t] = p[t];
-                if (i == 0) sc[t] = __fmul_rn(sb[t], sw);
+                b0[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c0);
+                b1[t] = *reinterpret_cast<lds_v4*>(from + brow + t * 2048 + c1);
+            }
+            const lds_t* row = tab + ((s >> 3) & 1) * kTab + (s & 7) * 4;
+            const float sw = *reinterpret_cast<lds_f*>(row + (BT + wm * (BW / WW) / 128) * 32);
+            float sb[SB];
+#pragma unroll
+            for (int t = 0; t < SB; ++t) sb[t] = *reinterpret_cast<lds_f*>(row + (wt * (BT / WT) + 16 * t + lr) * 32);
+            __builtin_amdgcn_sched_barrier(0);
+            issue_at_start(s);                                   // behind the first reads
+            __builtin_amdgcn_sched_barrier(0);
+            Op av(a0, a1), bv[SB];
+#pragma unroll
+            for (int t = 0; t < SB; ++t) bv[t] = Op(b0[t], b1[t]);
+#pragma unroll
+            for (int i = 0; i < SA; ++i) {
+                Op next;
+                f32x4 p[SB];
+                if (i + 1 < SA) {
+                    a0 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c0);
+                    a1 = *reinterpret_cast<lds_v4*>(from + arow + (i + 1) * 2048 + c1);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int t = 0; t < SB; ++t) {
+                        p[t] = mma(av.part[k], bv[t].part[k], k == 0 ? f32x4{0, 0, 0, 0} : p[t]);
+                        f32x4& to = acc[(i + SA - 1) % SA][t];
+                        to[k] = __builtin_fmaf(sc[t], prev[t][k], to[k]);
+                    }
+                    if (k >= 2 && i + 1 < SA) {                  // the next row's reads have had two parts' time
+                        const i32x4 c = k == 2 ? a0 : a1;
+                        next.part[2 * k - 4] = e4m3x8_to_bf16(c[0], c[1], 1.0f);
+                        next.part[2 * k - 3] = e4m3x8_to_bf16(c[2], c[3], 1.0f);
+                    }
+                    if (i > 0) __builtin_amdgcn_sched_barrier(0);
+                }
+                av = next;
+#pragma unroll
+                for (int t = 0; t < SB; ++t) {
+                    prev[t] = p[t];
+                    if (i == 0) sc[t] = __fmul_rn(sb[t], sw);
+                }
             }
         }
     };
@@ -287,10 +305,22 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     __syncthreads();
     constexpr int kCols = BW / WW;
     lds_t* const rows16 = ring + wv * (16 * kOutRow<kCols>);
+    const lds_t* const wscales = tab + 4 * (wm * kCols + 4 * lk);
+    const lds_t* const ascales = tab + 4 * (BW + wt * (BT / WT) + lr);
 #pragma unroll
     for (int t = 0; t < SB; ++t) {
+        float sa = 0.0f;
+        if constexpr (INT8) sa = *reinterpret_cast<lds_f*>(ascales + 64 * t);
 #pragma unroll
-        for (int i = 0; i < SA; ++i) stage4<kCols>(rows16, lr, 16 * i + 4 * lk, acc[i][t]);
+        for (int i = 0; i < SA; ++i) {
+            if constexpr (INT8) {
+                typedef const __attribute__((address_space(3))) f32x4 lds_f4;
+                stage4<kCols>(rows16, lr, 16 * i + 4 * lk,
+                              scaled(acc[i][t], sa, *reinterpret_cast<lds_f4*>(wscales + 64 * i)));
+            } else {
+                stage4<kCols>(rows16, lr, 16 * i + 4 * lk, acc[i][t]);
+            }
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         store_tile<kCols, 16, 64, BW == 256>(g, rows16, row0 + wt * (BT / WT) + 16 * t, row1, n0 + wm * kCols);
@@ -299,14 +329,14 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     }
 }
 
-template <bool FP8, int BW, int BT, int WW, int WT, int S, bool NTW>
+template <RowsKind KIND, int BW, int BT, int WW, int WT, int S, bool NTW>
 __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g, int ntiles, int band) {
     // The last block of a group, of half the rows or fewer: the room of the
     // missing ones goes into a third slot and all waves share the rest (20000
     // rows in 64 bf16 groups of 2000 x 1024 120 -> 115 us).
     constexpr bool kPart64 = BW == 256, kPart128 = BW == 256 && BT == 256;
-    constexpr int kLds = std::max({tile_lds<FP8, BW, BT, S>(), kPart64 ? tile_lds<FP8, BW, 64, 3>() : 0,
-                                   kPart128 ? tile_lds<FP8, BW, 128, 3>() : 0});
+    constexpr int kLds = std::max({tile_lds<KIND, BW, BT, S>(), kPart64 ? tile_lds<KIND, BW, 64, 3>() : 0,
+                                   kPart128 ? tile_lds<KIND, BW, 128, 3>() : 0});
     // one LDS object: with several, the compiler waits for every direct-to-LDS
     // load before each LDS read
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
@@ -327,42 +357,46 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
     if (!find_block<BT>(g, slot, e, row0, row1)) return;
 
     if constexpr (kPart64) {
-        if (row1 - row0 <= 64) return tile_product<FP8, BW, 64, 4, 2, 3, NTW>(g, ring, e, row0, row1, n0);
+        if (row1 - row0 <= 64) return tile_product<KIND, BW, 64, 4, 2, 3, NTW>(g, ring, e, row0, row1, n0);
     }
     if constexpr (kPart128) {
-        if (row1 - row0 <= 128) return tile_product<FP8, BW, 128, 4, 2, 3, NTW>(g, ring, e, row0, row1, n0);
+        if (row1 - row0 <= 128) return tile_product<KIND, BW, 128, 4, 2, 3, NTW>(g, ring, e, row0, row1, n0);
     }
-    tile_product<FP8, BW, BT, WW, WT, S, NTW>(g, ring, e, row0, row1, n0);
+    tile_product<KIND, BW, BT, WW, WT, S, NTW>(g, ring, e, row0, row1, n0);
 }
 
-template <bool FP8, int BW, int BT, int WW, int WT, int S>
+template <RowsKind KIND, int BW, int BT, int WW, int WT, int S>
 hipError_t launch_tile(const RowsGemmArgs& g, bool one_pass, hipStream_t s) {
     const int ntiles = (g.N + BW - 1) / BW;
     const int64_t slots = block_slots(g, BT);
     void (*kern)(RowsGemmArgs, int, int) =
-        one_pass ? rows_tile_kernel<FP8, BW, BT, WW, WT, S, true> : rows_tile_kernel<FP8, BW, BT, WW, WT, S, false>;
+        one_pass ? rows_tile_kernel<KIND, BW, BT, WW, WT, S, true> : rows_tile_kernel<KIND, BW, BT, WW, WT, S, false>;
     return start(kern, xcd_grid(slots * ntiles), 64 * WW * WT, s, g, ntiles, std::min(kBand, ntiles));
 }
 
-template <bool FP8>
+template <RowsKind KIND>
 hipError_t launch(const RowsGemmArgs& g, int shape, bool one_pass, hipStream_t s) {
     switch (shape) {
-        case 0: return launch_tile<FP8, 64, 32, 2, 2, 4>(g, one_pass, s);
-        case 1: return launch_tile<FP8, 128, 64, 4, 1, 3>(g, one_pass, s);
-        case 2: return launch_tile<FP8, 128, 128, 2, 4, 4>(g, one_pass, s);
-        case 3: return launch_tile<FP8, 256, 128, 4, 2, 3>(g, one_pass, s);
+        case 0: return launch_tile<KIND, 64, 32, 2, 2, 4>(g, one_pass, s);
+        case 1: return launch_tile<KIND, 128, 64, 4, 1, 3>(g, one_pass, s);
+        case 2: return launch_tile<KIND, 128, 128, 2, 4, 4>(g, one_pass, s);
+        case 3: return launch_tile<KIND, 256, 128, 4, 2, 3>(g, one_pass, s);
         default: break;
     }
-    if constexpr (!FP8) {                                    // of converted e4m3 operands: out of registers
-        if (shape == 4) return launch_tile<false, 256, 256, 2, 4, 2>(g, one_pass, s);
+    if constexpr (KIND != kRowsFp8) {                        // of converted e4m3 operands: out of registers
+        if (shape == 4) return launch_tile<KIND, 256, 256, 2, 4, 2>(g, one_pass, s);
     }
     return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_rows_tile(const RowsGemmArgs& g, bool fp8, int shape, bool one_pass, hipStream_t s) {
-    return fp8 ? launch<true>(g, shape, one_pass, s) : launch<false>(g, shape, one_pass, s);
+hipError_t launch_rows_tile(const RowsGemmArgs& g, RowsKind kind, int shape, bool one_pass, hipStream_t s) {
+    switch (kind) {
+        case kRowsBf16: return launch<kRowsBf16>(g, shape, one_pass, s);
+        case kRowsFp8: return launch<kRowsFp8>(g, shape, one_pass, s);
+        default: return launch<kRowsInt8>(g, shape, one_pass, s);
+    }
 }
 
 }  // namespace moe

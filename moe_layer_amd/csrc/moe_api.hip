@@ -15,11 +15,11 @@ using namespace moe;
 namespace {
 
 constexpr int kVersionMajor = 1;
-constexpr int kVersionMinor = 8;   // 1.1: MXFP8 weights; 1.2: layer variants; 1.3: moe_decode_layer;
+constexpr int kVersionMinor = 9;   // 1.1: MXFP8 weights; 1.2: layer variants; 1.3: moe_decode_layer;
                                    // 1.4: packed MXFP8 scales (moe_pack_mx_scales);
                                    // 1.5: multi-workgroup alignment (moe_align_ws);
                                    // 1.6: moe_forward_noalloc; 1.7: the operators around the layer;
-                                   // 1.8: moe_gemm_plan
+                                   // 1.8: moe_gemm_plan; 1.9: rows sorted by expert and back, int8
 // Rows per expert (on average) from which the LDS-tiled path beats weight
 // streaming.  Measured with bf16 weights (align + GEMM1 + GEMM2): E 128, H
 // 4096, I 1536 at 8 rows 0.90 ms streaming vs 1.08 tiled, 16 rows 1.14 vs 1.09,

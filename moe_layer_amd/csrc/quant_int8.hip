@@ -1,0 +1,86 @@
+// int8 quantisation of bf16 rows with one scale each, as they are or behind the
+// SiLU-gated multiply of a product's gate and up halves:
+//   m = max(|v|max, 1e-10), scale = fl32(m / 127), code = RNE(v fl32(127 / m)),
+//   gated: v = bf16(bf16(silu(g)) * u) after the optional clamp (dev_silu.h).
+//
+// A row is held in the registers of W waves, CH chunks of 8 columns a lane, so
+// it is read once; the maximum of the row's bf16 bits is joined through lane
+// permutations and, for W > 1, LDS.
+#include "moe.h"
+
+#include "dev_silu.h"
+#include "sorted.h"
+
+namespace moe {
+
+namespace {
+
+template <int W, int CH, bool kGated, bool kClamp>
+__global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void quant_int8_kernel(Int8Args a) {
+    constexpr int NT = W <= 4 ? 256 : 64 * W, kRows = NT / 64 / W;
+    __shared__ uint32_t s_max[NT / 64];
+    const int64_t wg = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t mine = wg * kRows + threadIdx.x / (64 * W);
+    if (W == 1 && mine >= a.rows) return;
+    const int64_t row = min(mine, int64_t(a.rows) - 1);
+    const int tid = threadIdx.x % (64 * W), nvec = a.cols >> 3;
+    const uint16_t* x = a.x + row * a.cols * (kGated ? 2 : 1);
+    i32x4 v[CH], u[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = min(tid + c * 64 * W, nvec - 1);     // behind the row: its last chunk again
+        v[c] = *reinterpret_cast<const i32x4*>(x + i * 8);
+        if constexpr (kGated) u[c] = *reinterpret_cast<const i32x4*>(x + a.cols + i * 8);
+    }
+    uint32_t most = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        if constexpr (kGated) v[c] = silu_mul8<kClamp>(v[c], u[c], a.limit);
+        most = pk_max_u16(most, abs_max8(v[c]));
+    }
+    uint32_t bits = wave_max_u16(most);
+    if constexpr (W > 1) {
+        if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = bits;
+        __syncthreads();
+        const int first = threadIdx.x / (64 * W) * W;
+#pragma unroll
+        for (int i = 0; i < W; ++i) bits = max(bits, s_max[first + i]);
+    }
+    float inverse;
+    const float scale = int8_scale(bits, inverse);
+    if (mine >= a.rows) return;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = tid + c * 64 * W;
+        if (i < nvec) *reinterpret_cast<uint2*>(a.codes + row * a.cols + i * 8) = int8_codes(v[c], inverse);
+    }
+    if (tid == 0) a.scales[row] = scale;
+}
+
+template <bool kGated, bool kClamp>
+hipError_t launch(const Int8Args& a, hipStream_t s) {
+    auto go = [&](auto w, auto ch) {
+        constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
+        constexpr int NT = W <= 4 ? 256 : 64 * W, kRows = NT / 64 / W;
+        return start(quant_int8_kernel<W, CH, kGated, kClamp>, grid_of((int64_t(a.rows) + kRows - 1) / kRows), NT, s, a);
+    };
+    using std::integral_constant;
+    const int nvec = a.cols >> 3;
+    if (nvec <= 64) return go(integral_constant<int, 1>(), integral_constant<int, 1>());
+    if (nvec <= 128) return go(integral_constant<int, 1>(), integral_constant<int, 2>());
+    if (nvec <= 256) return go(integral_constant<int, 4>(), integral_constant<int, 1>());
+    if (nvec <= 512) return go(integral_constant<int, 4>(), integral_constant<int, 2>());
+    if (nvec <= 1024) return go(integral_constant<int, 4>(), integral_constant<int, 4>());
+    if (nvec <= 2048) return go(integral_constant<int, 16>(), integral_constant<int, 2>());
+    static_assert(MOE_MAX_INT8_K <= 1024 * 4 * 8, "a row in one workgroup's registers");
+    return go(integral_constant<int, 16>(), integral_constant<int, 4>());
+}
+
+}  // namespace
+
+hipError_t launch_quant_int8(const Int8Args& a, bool gated, hipStream_t s) {
+    if (!gated) return launch<false, false>(a, s);
+    return a.limit > 0.0f ? launch<true, true>(a, s) : launch<true, false>(a, s);
+}
+
+}  // namespace moe

@@ -1,50 +1,16 @@
 // C ABI of the operators around the fused layer: argument checks and launches
-// of moe_rmsnorm, moe_silu_mul, moe_gemm_fp8 and moe_grouped_gemm (documented
-// in include/moe.h).
+// of moe_rmsnorm, moe_silu_mul, moe_gemm_fp8, moe_gemm_int8 and
+// moe_grouped_gemm (documented in include/moe.h).
 #include "moe.h"
 
 #include <cmath>
-#include <initializer_list>
 
+#include "api_checks.h"
 #include "dense.h"
 
 using namespace moe;
 
 namespace {
-
-constexpr int32_t kMaxRows = 1 << 30;   // row indices plus a block stay in 32 bits
-constexpr int32_t kMaxCols = 1 << 20;   // and byte counts in 64
-
-int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Span {
-    const void* p;
-    int64_t bytes;
-};
-bool overlap(const Span& a, const Span& b) {
-    if (!a.p || !b.p) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + uintptr_t(b.bytes) && b0 < a0 + uintptr_t(a.bytes);
-}
-// any output over an input or another output; each of the first `in_place` outputs
-// may be one of the first `in_place` inputs itself
-bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins, int in_place) {
-    int i = 0;
-    for (const Span& o : outs) {
-        int k = 0;
-        for (const Span& n : ins) {
-            const bool itself = i < in_place && k < in_place && o.p == n.p && o.bytes == n.bytes;
-            if (overlap(o, n) && !itself) return true;
-            ++k;
-        }
-        int j = 0;
-        for (const Span& other : outs)
-            if (j++ > i && overlap(o, other)) return true;
-        ++i;
-    }
-    return false;
-}
 
 // columns per scale of a quantised row, 0 for none, -1 for an unknown format
 int quant_group(int32_t quant) {
@@ -68,11 +34,29 @@ int check_codes(const uint8_t* codes, const void* scales, int group) {
 }
 
 int check_product(const void* a, const float* a_scale, const void* w, const float* w_scale, const void* out,
-                  bool fp8) {
+                  bool scaled) {
     if (!a || !w || !out || !aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16)) return MOE_ERR_INVALID_ARG;
-    if (fp8 ? !a_scale || !w_scale || !aligned(a_scale, 4) || !aligned(w_scale, 4) : a_scale || w_scale)
+    if (scaled ? !a_scale || !w_scale || !aligned(a_scale, 4) || !aligned(w_scale, 4) : a_scale || w_scale)
         return MOE_ERR_INVALID_ARG;
     return MOE_OK;
+}
+
+// the operands of a weight type; false for an unknown one
+bool rows_kind(int32_t wdtype, RowsKind& kind) {
+    switch (wdtype) {
+        case MOE_WDTYPE_BF16: kind = kRowsBf16; return true;
+        case MOE_WDTYPE_FP8_E4M3: kind = kRowsFp8; return true;
+        case MOE_WDTYPE_INT8: kind = kRowsInt8; return true;
+        default: return false;
+    }
+}
+// whether the products take rows of K elements
+bool fits_k(RowsKind kind, int32_t K) {
+    switch (kind) {
+        case kRowsBf16: return K % 64 == 0 && K <= kMaxCols;
+        case kRowsFp8: return K % MOE_QUANT_GROUP == 0 && K <= kMaxCols;
+        default: return K % 16 == 0 && K <= MOE_MAX_INT8_K;
+    }
 }
 
 }  // namespace
@@ -129,9 +113,9 @@ MOE_API int moe_silu_mul(const void* h, int32_t rows, int32_t cols, float clamp_
 MOE_API int moe_gemm_plan(int32_t rows, int32_t E, int32_t N, int32_t K, int32_t wdtype, moe_gemm_plan_info* out) {
     if (rows < 1 || E < 0 || E > MOE_MAX_EXPERTS || N <= 0 || K <= 0 || !out) return MOE_ERR_INVALID_ARG;
     if (wdtype == MOE_WDTYPE_MXFP8) return MOE_ERR_UNSUPPORTED;
-    if (wdtype != MOE_WDTYPE_BF16 && wdtype != MOE_WDTYPE_FP8_E4M3) return MOE_ERR_INVALID_ARG;
-    const bool fp8 = wdtype == MOE_WDTYPE_FP8_E4M3;
-    if ((E == 0 && !fp8) || K % (fp8 ? MOE_QUANT_GROUP : 64) != 0 || rows > kMaxRows || N > kMaxRows || K > kMaxCols)
+    RowsKind kind;
+    if (!rows_kind(wdtype, kind)) return MOE_ERR_INVALID_ARG;
+    if ((E == 0 && kind == kRowsBf16) || !fits_k(kind, K) || rows > kMaxRows || N > kMaxRows)
         return MOE_ERR_UNSUPPORTED;
     static const int32_t there = 0;   // the plan looks at no offset
     RowsGemmArgs g{};
@@ -140,7 +124,7 @@ MOE_API int moe_gemm_plan(int32_t rows, int32_t E, int32_t N, int32_t K, int32_t
     g.E = E > 0 ? E : 1;
     g.N = N;
     g.K = K;
-    const RowsPlan p = plan_rows_gemm(g, fp8);
+    const RowsPlan p = plan_rows_gemm(g, kind);
     *out = moe_gemm_plan_info{p.split, p.bw, p.bt, p.one_pass};
     return MOE_OK;
 }
@@ -167,7 +151,31 @@ MOE_API int moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* 
     g.E = 1;
     g.N = N;
     g.K = K;
-    return hip_status(launch_rows_gemm(g, true, stream));
+    return hip_status(launch_rows_gemm(g, kRowsFp8, stream));
+}
+
+MOE_API int moe_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale, int32_t M,
+                          int32_t N, int32_t K, void* out, hipStream_t stream) {
+    if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+    if (!fits_k(kRowsInt8, K) || M > kMaxRows || N > kMaxRows) return MOE_ERR_UNSUPPORTED;
+    if (M == 0) return MOE_OK;
+    const int st = check_product(a, a_scale, w, w_scale, out, true);
+    if (st != MOE_OK) return st;
+    if (clash({{out, 2 * int64_t(M) * N}},
+              {{a, int64_t(M) * K}, {a_scale, 4 * int64_t(M)}, {w, int64_t(N) * K}, {w_scale, 4 * int64_t(N)}}, 0))
+        return MOE_ERR_INVALID_ARG;
+    RowsGemmArgs g{};
+    g.a = reinterpret_cast<const uint8_t*>(a);
+    g.a_scale = a_scale;
+    g.w = reinterpret_cast<const uint8_t*>(w);
+    g.w_scale = w_scale;
+    g.offsets = nullptr;
+    g.out = static_cast<uint16_t*>(out);
+    g.rows = M;
+    g.E = 1;
+    g.N = N;
+    g.K = K;
+    return hip_status(launch_rows_gemm(g, kRowsInt8, stream));
 }
 
 MOE_API int moe_grouped_gemm(const void* a, const float* a_scale, const void* w, const float* w_scale,
@@ -175,17 +183,19 @@ MOE_API int moe_grouped_gemm(const void* a, const float* a_scale, const void* w,
                              void* out, hipStream_t stream) {
     if (rows < 0 || E < 1 || E > MOE_MAX_EXPERTS || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
     if (wdtype == MOE_WDTYPE_MXFP8) return MOE_ERR_UNSUPPORTED;
-    if (wdtype != MOE_WDTYPE_BF16 && wdtype != MOE_WDTYPE_FP8_E4M3) return MOE_ERR_INVALID_ARG;
-    const bool fp8 = wdtype == MOE_WDTYPE_FP8_E4M3;
-    if (K % (fp8 ? MOE_QUANT_GROUP : 64) != 0 || rows > kMaxRows || N > kMaxRows || K > kMaxCols)
-        return MOE_ERR_UNSUPPORTED;
+    RowsKind kind;
+    if (!rows_kind(wdtype, kind)) return MOE_ERR_INVALID_ARG;
+    if (!fits_k(kind, K) || rows > kMaxRows || N > kMaxRows) return MOE_ERR_UNSUPPORTED;
     if (rows == 0) return MOE_OK;
-    const int st = check_product(a, a_scale, w, w_scale, out, fp8);
+    const int st = check_product(a, a_scale, w, w_scale, out, kind != kRowsBf16);
     if (st != MOE_OK) return st;
     if (!offsets || !aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
-    const int64_t es = fp8 ? 1 : 2, kb = K / MOE_QUANT_GROUP, nb = (int64_t(N) + 127) / 128;
+    const int64_t es = kind == kRowsBf16 ? 2 : 1;
+    // scales of a row of a, and of an expert's weights
+    const int64_t sa = kind == kRowsFp8 ? K / MOE_QUANT_GROUP : 1;
+    const int64_t sw = kind == kRowsFp8 ? (int64_t(N) + 127) / 128 * (K / MOE_QUANT_GROUP) : N;
     if (clash({{out, 2 * int64_t(rows) * N}},
-              {{a, es * rows * K}, {a_scale, 4 * kb * rows}, {w, es * E * N * K}, {w_scale, 4 * kb * nb * E},
+              {{a, es * rows * K}, {a_scale, 4 * sa * rows}, {w, es * E * N * K}, {w_scale, 4 * sw * E},
                {offsets, 4 * (int64_t(E) + 1)}}, 0))
         return MOE_ERR_INVALID_ARG;
     RowsGemmArgs g{};
@@ -199,7 +209,7 @@ MOE_API int moe_grouped_gemm(const void* a, const float* a_scale, const void* w,
     g.E = E;
     g.N = N;
     g.K = K;
-    return hip_status(launch_rows_gemm(g, fp8, stream));
+    return hip_status(launch_rows_gemm(g, kind, stream));
 }
 
 }  // extern "C"

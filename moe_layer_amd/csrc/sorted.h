@@ -1,0 +1,106 @@
+// Launchers and shared device code of the operators that sort a batch by
+// expert and bring it back (sort_rows.hip, combine_rows.hip) and that quantise
+// rows to int8 (quant_int8.hip).
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "dense.h"
+
+namespace moe {
+
+// What moe_sort_rows does with a row on its way
+enum SortMode { kSortCopy, kSortInt8, kSortFp8 };
+
+struct SortArgs {
+    const uint8_t* x;          // [T, row_bytes]
+    const float* x_scale;      // [T, scales] (codes) or null
+    const int32_t* ids;        // [T, topk]
+    uint8_t* rows;             // [T * topk] rows of row_bytes (copy) or cols codes
+    float* row_scales;         // [T * topk, scales] or null
+    int32_t* offsets;          // [E + 1]
+    int32_t* inv;              // [T, topk]
+    int32_t* counts;           // scratch [blocks, E]
+    int T, topk, E, R;         // R = T * topk
+    int cols;
+    int units;                 // 16-byte pieces of a source row
+    int scales;                // scales of a row that is copied or made
+};
+// slots per block of the counted form, and its blocks; 0 blocks where the
+// positions are found without counts
+struct SortPlan {
+    int slots, blocks;
+};
+SortPlan plan_sort(int64_t R, int E);
+hipError_t launch_sort_rows(const SortArgs& a, SortMode mode, hipStream_t s);
+
+struct CombineArgs {
+    const uint16_t* rows;      // bf16 [num_rows, cols]
+    const int32_t* inv;        // [T, topk]
+    const float* weights;      // [T, topk] or null
+    uint16_t* out;             // bf16 [T, cols]
+    const uint16_t* grad_out;  // bf16 [T, cols]
+    uint16_t* grad_rows;       // bf16 [num_rows, cols]
+    float* grad_weights;       // [T, topk] or null
+    int T, topk, cols, num_rows;
+};
+hipError_t launch_combine_rows(const CombineArgs& a, hipStream_t s);
+hipError_t launch_combine_rows_bwd(const CombineArgs& a, hipStream_t s);
+
+struct Int8Args {
+    const uint16_t* x;         // bf16 [rows, cols], gated: [rows, 2 cols]
+    int8_t* codes;             // [rows, cols]
+    float* scales;             // [rows]
+    int rows, cols;
+    float limit;
+};
+hipError_t launch_quant_int8(const Int8Args& a, bool gated, hipStream_t s);
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// int8 rows: m = max(|v|max, 1e-10), scale = fl32(m / 127), and the code of v
+// the whole number nearest to v fl32(127 / m) (ties to even; at most 127)
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t abs_max8(const i32x4& w) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    return pk_max_u16(pk_max_u16(uint32_t(w[0]) & kAbs, uint32_t(w[1]) & kAbs),
+                      pk_max_u16(uint32_t(w[2]) & kAbs, uint32_t(w[3]) & kAbs));
+}
+// the largest half of a wave's words, in every lane; the bits of a bf16 without
+// their sign order as the magnitudes do
+__device__ __forceinline__ uint32_t wave_max_u16(uint32_t m) {
+    m = dpp_max_u16<0xb1>(m);                              // quad_perm [1,0,3,2]
+    m = dpp_max_u16<0x4e>(m);                              // quad_perm [2,3,0,1]
+    m = dpp_max_u16<0x141>(m);                             // row_half_mirror
+    m = dpp_max_u16<0x140>(m);                             // row_mirror
+    const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = pk_max_u16(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    m = pk_max_u16(b[0], b[1]);
+    return max(m & 0xffffu, m >> 16);
+}
+// scale and inverse from the row's largest magnitude (its bf16 bits); a row with
+// an infinity or a NaN gets the scale NaN, so what is made of it is NaN
+__device__ __forceinline__ float int8_scale(uint32_t bits, float& inverse) {
+    const float m = fmaxf(__uint_as_float(bits << 16), 1e-10f);
+    inverse = __fdiv_rn(127.0f, m);
+    return bits >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __fdiv_rn(m, 127.0f);
+}
+// codes of 8 packed bf16 values.  v inverse + 1.5 2^23 is rounded once, to a whole
+// number (ties to even), whose low byte is the code.
+__device__ __forceinline__ uint2 int8_codes(const i32x4& w, float inverse) {
+    constexpr float kWhole = 12582912.0f;
+    uint32_t pair[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        pair[q] = __builtin_amdgcn_perm(__float_as_uint(__builtin_fmaf(bf16_hi(w[q]), inverse, kWhole)),
+                                        __float_as_uint(__builtin_fmaf(bf16_lo(w[q]), inverse, kWhole)), 0x0c0c0400u);
+    return uint2{pair[0] | pair[1] << 16, pair[2] | pair[3] << 16};
+}
+
+}  // namespace
+
+}  // namespace moe

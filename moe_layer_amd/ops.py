@@ -19,10 +19,11 @@ _LIB_PATH = os.environ.get("MOE_MI355X_LIB") or os.path.join(os.path.dirname(os.
 _lib = None
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1, -2, -3, -4
-MOE_WDTYPE_BF16, MOE_WDTYPE_FP8_E4M3, MOE_WDTYPE_MXFP8 = 0, 1, 2
+MOE_WDTYPE_BF16, MOE_WDTYPE_FP8_E4M3, MOE_WDTYPE_MXFP8, MOE_WDTYPE_INT8 = 0, 1, 2, 4
 MOE_PATH_AUTO, MOE_PATH_SMALL_M, MOE_PATH_LARGE_M = 0, 1, 2
 MOE_FLAG_WEIGHT_ON_INPUT, MOE_FLAG_MX_PACKED_SCALES = 1, 2
 MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_QUANT_GROUP, MOE_MX_BLOCK = 1024, 64, 128, 32
+MOE_MAX_INT8_K = 32768
 
 # every entry point include/moe.h declares
 EXPORTS = ("moe_status_string", "moe_version", "moe_route", "moe_align_capacity", "moe_align",
@@ -30,7 +31,8 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route", "moe_align_capacity"
            "moe_quant_act", "moe_quant_act_mx", "moe_pack_mx_scales", "moe_plan", "moe_forward_workspace", "moe_forward",
            "moe_forward_profiled", "moe_decode_layer", "moe_forward_noalloc",
            "moe_rmsnorm", "moe_silu_mul", "moe_gemm_fp8", "moe_grouped_gemm",
-           "moe_gemm_plan")
+           "moe_gemm_plan", "moe_gemm_int8", "moe_quant_act_int8", "moe_silu_mul_int8",
+           "moe_sort_scratch_bytes", "moe_sort_rows", "moe_combine_rows", "moe_combine_rows_bwd")
 MOE_NUM_STAGES = 5
 MOE_NOALLOC_MAX_BYTES = 64 << 20
 MOE_SYNC_WORDS, MOE_SYNC_ERROR = 640, 576
@@ -113,6 +115,20 @@ def lib() -> C.CDLL:
         L.moe_gemm_fp8.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp]
         L.moe_grouped_gemm.restype = C.c_int
         L.moe_grouped_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+        L.moe_gemm_int8.restype = C.c_int
+        L.moe_gemm_int8.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp]
+        L.moe_quant_act_int8.restype = C.c_int
+        L.moe_quant_act_int8.argtypes = [vp, i32, i32, vp, vp, vp]
+        L.moe_silu_mul_int8.restype = C.c_int
+        L.moe_silu_mul_int8.argtypes = [vp, i32, i32, C.c_float, vp, vp, vp]
+        L.moe_sort_scratch_bytes.restype = i64
+        L.moe_sort_scratch_bytes.argtypes = [i32, i32, i32]
+        L.moe_sort_rows.restype = C.c_int
+        L.moe_sort_rows.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i64, vp]
+        L.moe_combine_rows.restype = C.c_int
+        L.moe_combine_rows.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp]
+        L.moe_combine_rows_bwd.restype = C.c_int
+        L.moe_combine_rows_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]
         L.moe_gemm_plan.restype = C.c_int
         L.moe_gemm_plan.argtypes = [i32, i32, i32, i32, i32, C.POINTER(GemmPlanInfo)]
         _lib = L
@@ -429,8 +445,10 @@ def _binding():
             raise RuntimeError("the package's native binding is missing or does not load: build it with "
                                "`python -m moe_layer_amd.build`") from e
         L = lib()
-        m.bind(*(C.cast(f, C.c_void_p).value for f in (L.moe_rmsnorm, L.moe_silu_mul, L.moe_gemm_fp8,
-                                                       L.moe_grouped_gemm)))
+        m.bind(*(C.cast(f, C.c_void_p).value for f in (
+            L.moe_rmsnorm, L.moe_silu_mul, L.moe_gemm_fp8, L.moe_grouped_gemm, L.moe_gemm_int8, L.moe_quant_act_int8,
+            L.moe_silu_mul_int8, L.moe_sort_rows, L.moe_sort_scratch_bytes, L.moe_combine_rows,
+            L.moe_combine_rows_bwd)))
         _current_device = getattr(torch._C, "_cuda_getDevice", None)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _native = m
@@ -490,19 +508,85 @@ def moe_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scal
     return _call("gemm_fp8", a, a_scale, w, w_scale, out)
 
 
+def moe_gemm_int8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                  out=None) -> torch.Tensor:
+    """Dense product of 8-bit integers with a scale per token and per output
+    channel: int8 a [M, K] with fp32 a_scale [M], int8 w [N, K] with fp32 w_scale
+    [N]; returns bf16 out [M, N]."""
+    return _call("gemm_int8", a, a_scale, w, w_scale, out)
+
+
+def moe_quant_act_int8(x: torch.Tensor, codes=None, scales=None):
+    """bf16 rows [rows, cols] as int8 codes with one fp32 scale per row; returns
+    (codes int8 [rows, cols], scales fp32 [rows])."""
+    return _call("quant_act_int8", x, codes, scales)
+
+
+def moe_silu_mul_int8(h: torch.Tensor, clamp_limit: float = 0.0, codes=None, scales=None):
+    """moe_silu_mul of bf16 h [rows, 2 * cols], quantised as moe_quant_act_int8
+    does; returns (codes int8 [rows, cols], scales fp32 [rows])."""
+    return _call("silu_mul_int8", h, clamp_limit, codes, scales)
+
+
 def moe_grouped_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, a_scale=None, w_scale=None,
                      out=None) -> torch.Tensor:
     """Products of rows sorted by expert, group e being rows offsets[e] ..
     offsets[e+1] (int32 [E+1] on the device): bf16 a [rows, K] and w [E, N, K],
-    or e4m3 ones with fp32 a_scale [rows, K/128] and w_scale [E, ceil(N/128),
-    K/128].  Returns bf16 out [rows, N]; rows outside every group keep what
+    e4m3 ones with fp32 a_scale [rows, K/128] and w_scale [E, ceil(N/128),
+    K/128], or int8 ones with fp32 a_scale [rows] and w_scale [E, N].  Returns bf16 out [rows, N]; rows outside every group keep what
     out held (uninitialised when it is allocated here)."""
     return _call("grouped_gemm", a, w, offsets, a_scale, w_scale, out)
 
 
 def moe_gemm_plan(rows: int, N: int, K: int, E: int = 0, wdtype: int = MOE_WDTYPE_FP8_E4M3) -> dict:
-    """Which kernel moe_gemm_fp8 (E = 0) or moe_grouped_gemm (E experts) takes
-    for these sizes (host only)."""
+    """Which kernel moe_gemm_fp8 or moe_gemm_int8 (E = 0) or moe_grouped_gemm (E
+    experts) takes for these sizes (host only)."""
     info = GemmPlanInfo()
     _check("moe_gemm_plan", lib().moe_gemm_plan(rows, E, N, K, wdtype, C.byref(info)))
     return {name: getattr(info, name) for name, _ in GemmPlanInfo._fields_}
+
+
+_ROW_TYPE = {None: -1, "fp8": MOE_WDTYPE_FP8_E4M3, "int8": MOE_WDTYPE_INT8}
+
+
+def moe_sort_scratch_bytes(T: int, topk: int, E: int) -> int:
+    n = lib().moe_sort_scratch_bytes(T, topk, E)
+    if n < 0:
+        raise MoeError("moe_sort_scratch_bytes", int(n))
+    return int(n)
+
+
+def moe_sort_rows(x: torch.Tensor, topk_ids: torch.Tensor, E: int, x_scale=None, quant=None, rows=None, scales=None,
+                  offsets=None, inv=None, scratch=None):
+    """Tokens' rows sorted by the expert they go to, one row for each routed slot
+    of int32 topk_ids [T, topk], as moe_grouped_gemm takes them.  x [T, cols] is
+    bf16, copied or quantised on the way (``quant`` "fp8": moe_quant_act's codes
+    and scales, "int8": moe_quant_act_int8's), or codes already: e4m3 with fp32
+    x_scale [T, cols/128], int8 with fp32 x_scale [T].  Outputs (and scratch:
+    uint8, moe_sort_scratch_bytes of it) that are not given are allocated.
+    Returns (rows [T * topk, cols], scales, offsets int32 [E+1], inv int32 [T,
+    topk]): slot (t, j) is row inv[t, j], -1 when its id is outside [0, E);
+    scales is None for bf16 rows.  Rows from offsets[E] on keep what they held
+    (uninitialised when allocated here)."""
+    if quant not in _ROW_TYPE:
+        raise AssertionError(f"quant: {quant!r}, expected None, 'fp8' or 'int8'")
+    return _call("sort_rows", x, topk_ids, E, x_scale, _ROW_TYPE[quant], rows, scales, offsets, inv, scratch)
+
+
+def moe_combine_rows(rows: torch.Tensor, inv: torch.Tensor, weights=None, out=None) -> torch.Tensor:
+    """The experts' bf16 rows [num_rows, cols] back at their tokens: out[t] =
+    sum_j weights[t, j] rows[inv[t, j]] with inv from moe_sort_rows and fp32
+    weights [T, topk] (None: 1, which makes it the gradient of moe_sort_rows with
+    respect to a bf16 x).  Returns bf16 out [T, cols]."""
+    return _call("combine_rows", rows, inv, weights, out)
+
+
+def moe_combine_rows_bwd(grad_out: torch.Tensor, inv: torch.Tensor, rows=None, weights=None, grad_rows=None,
+                         grad_weights=None):
+    """The gradients of moe_combine_rows given bf16 grad_out [T, cols]: bf16
+    grad_rows[inv[t, j]] = weights[t, j] grad_out[t], and where ``rows`` is given
+    fp32 grad_weights[t, j] = grad_out[t] . rows[inv[t, j]].  grad_rows has as
+    many rows as ``rows`` (without them T * topk when allocated here); rows that
+    no slot has keep what they held (uninitialised when allocated here).
+    Returns (grad_rows, grad_weights or None)."""
+    return _call("combine_rows_bwd", grad_out, inv, rows, weights, grad_rows, grad_weights)
