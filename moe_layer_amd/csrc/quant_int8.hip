@@ -57,6 +57,9 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void quant_int8_kernel(Int8A
     if (tid == 0) a.scales[row] = scale;
 }
 
+// Rows from which a wave takes a whole row
+constexpr int kManyRows = 2048;
+
 template <bool kGated, bool kClamp>
 hipError_t launch(const Int8Args& a, hipStream_t s) {
     auto go = [&](auto w, auto ch) {
@@ -65,15 +68,25 @@ hipError_t launch(const Int8Args& a, hipStream_t s) {
         return start(quant_int8_kernel<W, CH, kGated, kClamp>, grid_of((int64_t(a.rows) + kRows - 1) / kRows), NT, s, a);
     };
     using std::integral_constant;
+    using One = integral_constant<int, 1>;
+    using Four = integral_constant<int, 4>;
+    using Sixteen = integral_constant<int, 16>;
     const int nvec = a.cols >> 3;
-    if (nvec <= 64) return go(integral_constant<int, 1>(), integral_constant<int, 1>());
-    if (nvec <= 128) return go(integral_constant<int, 1>(), integral_constant<int, 2>());
-    if (nvec <= 256) return go(integral_constant<int, 4>(), integral_constant<int, 1>());
-    if (nvec <= 512) return go(integral_constant<int, 4>(), integral_constant<int, 2>());
-    if (nvec <= 1024) return go(integral_constant<int, 4>(), integral_constant<int, 4>());
-    if (nvec <= 2048) return go(integral_constant<int, 16>(), integral_constant<int, 2>());
+    if (a.rows >= kManyRows) {
+        if (nvec <= 64) return go(One(), One());
+        if (nvec <= 128) return go(One(), integral_constant<int, 2>());
+        if (nvec <= 192) return go(One(), integral_constant<int, 3>());
+        if (nvec <= 256) return go(One(), Four());
+        if (nvec <= 384) return go(One(), integral_constant<int, 6>());
+        if (nvec <= 512) return go(One(), integral_constant<int, 8>());
+    }
+    if (nvec <= 64) return go(One(), One());
+    if (nvec <= 256) return go(Four(), One());
+    if (nvec <= 512) return go(Four(), integral_constant<int, 2>());
+    if (nvec <= 1024) return go(Four(), Four());
+    if (nvec <= 2048) return go(Sixteen(), integral_constant<int, 2>());
     static_assert(MOE_MAX_INT8_K <= 1024 * 4 * 8, "a row in one workgroup's registers");
-    return go(integral_constant<int, 16>(), integral_constant<int, 4>());
+    return go(Sixteen(), Four());
 }
 
 }  // namespace

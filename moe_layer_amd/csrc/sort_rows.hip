@@ -4,11 +4,14 @@
 //   rows[inv[f]] = x[t] for the routed slots f = t topk + j, inv[f] = -1 for the others.
 // The position of a slot is the number of routed slots before it in the order
 // (expert, slot), so it is the same whichever form finds it:
-//   few slots   in the launch that moves the rows: every workgroup counts the
-//               slots before its token's own over all ids;
-//   many slots  blocks of slots are counted by expert (sort_count_kernel), every
-//               block adds the counts before its own and ranks its slots with a
-//               ballot multisplit (sort_place_kernel), then the rows are moved.
+//   few ids     every workgroup that moves a row compares its token's slots with
+//               all ids (sort_move_kernel<.., true>);
+//   batch       every workgroup counts all ids by expert in LDS, for several
+//               tokens at a time (sort_batch_kernel);
+//   counted     blocks of slots are counted by expert (sort_count_kernel), every
+//               block adds the counts before its own and ranks its slots
+//               (sort_place_kernel), then the rows are moved: three launches, for
+//               more ids than every workgroup should read.
 // A row is read once and stored topk times.
 #include "dev_align.h"
 #include "moe.h"
@@ -20,8 +23,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kOneLaunchSlots = 2048;
+constexpr int kBatchMostSlots = 32768;
 constexpr int kMostBlocks = 256;
+// tokens of a workgroup of the batch form: a whole number to each wave, about 512
+// workgroups
+constexpr int batch_tokens(int T) { return (T + 2047) / 2048 * 4; }
+// and its slots, at most kBatchMostSlots / 512 of T / 512 tokens and those of 4 more
+constexpr int kBatchSlots = kBatchMostSlots / 512 + 4 * MOE_MAX_TOPK;
 
 template <int CTRL>
 __device__ __forceinline__ int dpp_add(int v) {
@@ -59,6 +67,32 @@ __device__ __forceinline__ int scan_start(const int (&v)[PER], int* s) {
     return before + sum - mine;
 }
 
+// f(i, ids[i]) for every i below R, by NT threads: 16-byte loads, kFlight of them in
+// flight, and single ones in front of the first 16-byte border and behind the last
+template <int NT, int kFlight, typename F>
+__device__ __forceinline__ void each_id(const int32_t* ids, int R, int tid, F f) {
+    const int head = min(R, int(-(reinterpret_cast<uintptr_t>(ids) >> 2) & 3)), quads = (R - head) >> 2;
+    const i32x4* four = reinterpret_cast<const i32x4*>(ids + head);
+    for (int q0 = 0; q0 < quads; q0 += NT * kFlight) {
+        i32x4 v[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) v[u] = four[min(q0 + u * NT + tid, quads - 1)];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int q = q0 + u * NT + tid;
+            if (q < quads) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) f(head + 4 * q + w, v[u][w]);
+            }
+        }
+    }
+    const int rest = R - 4 * quads;                        // in front and behind, 6 at most
+    if (tid < rest) {
+        const int i = tid < head ? tid : tid + 4 * quads;
+        f(i, ids[i]);
+    }
+}
+
 // offsets of all experts by one workgroup of NT threads
 template <int NT>
 __device__ __forceinline__ void write_offsets(const SortArgs& a) {
@@ -67,10 +101,9 @@ __device__ __forceinline__ void write_offsets(const SortArgs& a) {
     __shared__ int s_scan[NT / 64];
     for (int e = threadIdx.x; e < kMaxE; e += NT) count[e] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.R; i += NT) {
-        const uint32_t e = uint32_t(a.ids[i]);
-        if (e < uint32_t(a.E)) atomicAdd(&count[e], 1);
-    }
+    each_id<NT, 2>(a.ids, a.R, threadIdx.x, [&](int, int id) {
+        if (uint32_t(id) < uint32_t(a.E)) atomicAdd(&count[id], 1);
+    });
     __syncthreads();
     int n[kPer];
 #pragma unroll
@@ -85,30 +118,55 @@ __device__ __forceinline__ void write_offsets(const SortArgs& a) {
     if (a.E == kMaxE && threadIdx.x == NT - 1) a.offsets[kMaxE] = at;
 }
 
-// positions of token t's slots into pos[topk], by all waves of the workgroup
+// positions of token t's slots into pos[topk] (set to 0 before, with a barrier),
+// eight slots at a time, every wave counting over its share of the ids
 template <int NT>
 __device__ __forceinline__ void find_positions(const SortArgs& a, int t, int* pos) {
-    constexpr int kNW = NT / 64, kAt = 4;
-    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (int j0 = wv; j0 < a.topk; j0 += kAt * kNW) {
+    constexpr int kAt = 8;
+    const int lane = threadIdx.x & 63, own = t * a.topk;
+    for (int j0 = 0; j0 < a.topk; j0 += kAt) {
         uint32_t e[kAt];
-        int f[kAt], n[kAt];
+        int n[kAt];
 #pragma unroll
         for (int q = 0; q < kAt; ++q) {
-            f[q] = t * a.topk + min(j0 + q * kNW, a.topk - 1);
-            e[q] = uint32_t(a.ids[f[q]]);
+            e[q] = uint32_t(a.ids[own + min(j0 + q, a.topk - 1)]);
             n[q] = 0;
         }
-#pragma unroll 4
-        for (int i = lane; i < a.R; i += 64) {
-            const uint32_t id = uint32_t(a.ids[i]);         // an unrouted one is past every expert
+        // a slot before counts where its expert is not above, one from the slot on
+        // where it is below; an unrouted id is above every expert
+        each_id<NT, 2>(a.ids, a.R, threadIdx.x, [&](int i, int id) {
 #pragma unroll
-            for (int q = 0; q < kAt; ++q) n[q] += id < e[q] + (i < f[q] ? 1u : 0u) ? 1 : 0;
-        }
+            for (int q = 0; q < kAt; ++q) n[q] += uint32_t(id) < e[q] + (i < own + j0 + q ? 1u : 0u) ? 1 : 0;
+        });
 #pragma unroll
         for (int q = 0; q < kAt; ++q) {
             const int sum = wave_sum(n[q]);
-            if (lane == 0 && j0 + q * kNW < a.topk) pos[j0 + q * kNW] = e[q] < uint32_t(a.E) ? sum : -1;
+            if (lane == q && j0 + q < a.topk) atomicAdd(&pos[j0 + q], e[q] < uint32_t(a.E) ? sum : -1);
+        }
+    }
+}
+
+// inv of slots first .. last - 1 by one wave, given each expert's next position;
+// also into pos[0 ..] where that is not null
+__device__ __forceinline__ void place_slots(const SortArgs& a, int first, int last, int* next, int* pos) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t lower = (uint64_t(1) << lane) - 1;
+    const int bits = a.E > 1 ? 32 - __clz(a.E - 1) : 0;
+    for (int i = first; i < last; i += 64) {
+        const int f = i + lane;
+        const int e = f < last ? a.ids[f] : -1;
+        const bool routed = uint32_t(e) < uint32_t(a.E);
+        const uint64_t same = peers(e, routed, bits);
+        int at = -1;
+        if (routed) {
+            const int to = next[e];
+            at = to + __popcll(same & lower);
+            // every lane's read of next[e] precedes the first one's update (one wave, in order)
+            if ((same & lower) == 0) next[e] = to + __popcll(same);
+        }
+        if (f < last) {
+            a.inv[f] = at;
+            if (pos) pos[f - first] = at;
         }
     }
 }
@@ -136,8 +194,6 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortArgs a, int sl
     __shared__ int before[kMaxE], total[kMaxE];
     __shared__ int s_scan[kWaves];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const uint64_t lower = (uint64_t(1) << lane) - 1;
-    const int bits = a.E > 1 ? 32 - __clz(a.E - 1) : 0;
     for (int i = threadIdx.x; i < kWaves * a.E; i += kThreads) run[i] = 0;
     for (int e = threadIdx.x; e < kMaxE; e += kThreads) before[e] = total[e] = 0;
     __syncthreads();
@@ -185,24 +241,71 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortArgs a, int sl
     }
     if (blockIdx.x == 0 && a.E == kMaxE && threadIdx.x == kThreads - 1) a.offsets[kMaxE] = at;
     __syncthreads();
-    for (int i = first; i < last; i += 64) {
-        const int f = i + lane;
-        const int e = f < last ? a.ids[f] : -1;
-        const bool routed = uint32_t(e) < uint32_t(a.E);
-        const uint64_t same = peers(e, routed, bits);
-        if (routed) {
-            const int to = mine[e];
-            a.inv[f] = to + __popcll(same & lower);
-            // every lane's read of mine[e] precedes the first one's update (one wave, in order)
-            if ((same & lower) == 0) mine[e] = to + __popcll(same);
-        } else if (f < last) {
-            a.inv[f] = -1;
+    place_slots(a, first, last, mine, nullptr);
+}
+
+// ---------------------------------------------------------------------------
+// rows on their way: pieces of 16 bytes (copied) or of 16 columns (quantised),
+// which leave as 16 bytes either way
+// ---------------------------------------------------------------------------
+template <SortMode kMode>
+struct Piece {
+    static constexpr int kLoads = kMode == kSortCopy ? 1 : 2;
+    i32x4 v[kLoads];
+    __device__ __forceinline__ void load(const uint8_t* row, int u) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            v[i] = *reinterpret_cast<const i32x4*>(row + int64_t(u * kLoads + i) * 16);
+    }
+};
+
+// the row's pieces u0, u0 + stride, .. below u1 (CH of them in p) to the
+// positions of the token's slots.  kSortInt8: bits is the row's largest magnitude;
+// kSortFp8: a lane's piece and its neighbours' make whole groups.
+template <SortMode kMode, int CH>
+__device__ __forceinline__ void store_pieces(const SortArgs& a, const Piece<kMode> (&p)[CH], const int* pos, int u0,
+                                             int u1, int stride, uint32_t bits) {
+    i32x4 out[CH];
+    float s[CH], inverse = 0.0f;
+    if constexpr (kMode == kSortInt8) s[0] = int8_scale(bits, inverse);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        if constexpr (kMode == kSortCopy) {
+            out[c] = p[c].v[0];
+        } else if constexpr (kMode == kSortInt8) {
+            const uint2 lo = int8_codes(p[c].v[0], inverse), hi = int8_codes(p[c].v[1], inverse);
+            out[c] = i32x4{int(lo.x), int(lo.y), int(hi.x), int(hi.y)};
+        } else {
+            s[c] = quant16(p[c].v[0], p[c].v[1], out[c]);
         }
+    }
+    for (int j = 0; j < a.topk; ++j) {
+        const int at = __builtin_amdgcn_readfirstlane(pos[j]);
+        if (at < 0) continue;
+        uint8_t* to = a.rows + int64_t(at) * a.units * 16;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int u = u0 + c * stride;
+            if (u < u1) {
+                *reinterpret_cast<i32x4*>(to + int64_t(u) * 16) = out[c];
+                if (kMode == kSortFp8 && (u & 7) == 0) a.row_scales[int64_t(at) * a.scales + (u >> 3)] = s[c];
+            }
+        }
+        if (kMode == kSortInt8 && u0 == 0) a.row_scales[at] = s[0];
     }
 }
 
-// A token's row (kSortInt8) or a part of it to the positions of its slots.
-// kOne: the positions are found here, and one more workgroup writes the offsets.
+// the scales of a token's codes, by `lanes` lanes
+__device__ __forceinline__ void copy_scales(const SortArgs& a, int64_t token, const int* pos, int lane, int lanes) {
+    for (int i = lane; i < a.scales; i += lanes) {
+        const float s = a.x_scale[token * a.scales + i];
+        for (int j = 0; j < a.topk; ++j)
+            if (pos[j] >= 0) a.row_scales[int64_t(pos[j]) * a.scales + i] = s;
+    }
+}
+
+// A token's row (kSortInt8) or a part of it by a workgroup.  kOne: the positions
+// are found here, and one more workgroup writes the offsets.
 template <SortMode kMode, int NT, int CH, bool kOne>
 __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, int span) {
     __shared__ int pos[MOE_MAX_TOPK];
@@ -215,14 +318,13 @@ __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, in
     }
     const int t = int(token), part = int(wg - token * parts);
     const int u0 = part * span + threadIdx.x, u1 = min(a.units, (part + 1) * span);
-    i32x4 v[CH];
-    const uint8_t* src = a.x + token * a.units * 16;
+    Piece<kMode> p[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {                         // behind the part: its last piece again
-        const int u = min(u0 + c * NT, u1 - 1);
-        v[c] = *reinterpret_cast<const i32x4*>(src + int64_t(u) * 16);
-    }
+    for (int c = 0; c < CH; ++c)                           // behind the part: its last piece again
+        p[c].load(a.x + token * a.units * (16 * Piece<kMode>::kLoads), min(u0 + c * NT, u1 - 1));
     if constexpr (kOne) {
+        if (threadIdx.x < unsigned(a.topk)) pos[threadIdx.x] = 0;
+        __syncthreads();
         find_positions<NT>(a, t, pos);
     } else {
         if (threadIdx.x < unsigned(a.topk)) pos[threadIdx.x] = a.inv[token * a.topk + threadIdx.x];
@@ -230,88 +332,147 @@ __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, in
     uint32_t bits = 0;
     if constexpr (kMode == kSortInt8) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) bits = pk_max_u16(bits, abs_max8(v[c]));
+        for (int c = 0; c < CH; ++c) bits = pk_max_u16(bits, pk_max_u16(abs_max8(p[c].v[0]), abs_max8(p[c].v[1])));
         bits = wave_max_u16(bits);
         if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = bits;
     }
     __syncthreads();
-    if (kOne && part == 0 && threadIdx.x < unsigned(a.topk)) a.inv[token * a.topk + threadIdx.x] = pos[threadIdx.x];
-    if constexpr (kMode == kSortCopy) {
-        for (int j = 0; j < a.topk; ++j) {
-            const int p = __builtin_amdgcn_readfirstlane(pos[j]);
-            if (p < 0) continue;
-            uint8_t* to = a.rows + int64_t(p) * a.units * 16;
+    if (kOne && part == 0 && threadIdx.x < unsigned(a.topk))
+        a.inv[token * a.topk + threadIdx.x] = max(pos[threadIdx.x], -1);
+    if constexpr (kMode == kSortInt8) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int u = u0 + c * NT;
-                if (u < u1) *reinterpret_cast<i32x4*>(to + int64_t(u) * 16) = v[c];
+        for (int i = 0; i < NT / 64; ++i) bits = max(bits, s_max[i]);
+    }
+    store_pieces<kMode, CH>(a, p, pos, u0, u1, NT, bits);
+    if (kMode == kSortCopy && part == 0) copy_scales(a, token, pos, threadIdx.x, NT);
+}
+
+// Tokens first .. first + per - 1 by a workgroup, a wave to a token's row or, of
+// long rows that are not int8's, a part of `span` pieces of it.
+// The workgroup counts all ids by expert, those before its own slots apart, in
+// `1 << rep` copies (lanes of one expert add to different ones), and ranks its
+// own slots; its first rows are on their way meanwhile.
+template <SortMode kMode, int CH>
+__global__ __launch_bounds__(kThreads) void sort_batch_kernel(SortArgs a, int per, int rep, int span) {
+    constexpr int kPer = kMaxE / kThreads;
+    __shared__ int count[2 * kMaxE];        // [before, from][E][1 << rep], then a slot's next position in each expert
+    __shared__ int pos[kBatchSlots];
+    __shared__ int s_scan[kWaves];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int first = blockIdx.x * per, last = min(a.T, first + per);
+    const int64_t row_bytes = int64_t(a.units) * (16 * Piece<kMode>::kLoads);
+    const int u0 = int(blockIdx.y) * span, u1 = min(a.units, u0 + span);
+    Piece<kMode> p[CH];
+    auto load = [&](int t, int u) {                        // behind the part: its last piece again
+#pragma unroll
+        for (int c = 0; c < CH; ++c) p[c].load(a.x + t * row_bytes, min(u + lane + 64 * c, u1 - 1));
+    };
+    load(min(first + wv, a.T - 1), u0);
+
+    for (int i = threadIdx.x; i < 2 * kMaxE; i += kThreads) count[i] = 0;
+    __syncthreads();
+    const int own = first * a.topk, copy = lane & ((1 << rep) - 1);
+    each_id<kThreads, 8>(a.ids, a.R, threadIdx.x, [&](int i, int id) {
+        if (uint32_t(id) < uint32_t(a.E)) atomicAdd(&count[((i >= own ? a.E : 0) + id << rep) + copy], 1);
+    });
+    __syncthreads();
+    int before[kPer], n[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        before[i] = n[i] = 0;
+        if (e < a.E)
+            for (int r = 0; r < 1 << rep; ++r) {
+                before[i] += count[(e << rep) + r];
+                n[i] += count[(a.E + e << rep) + r];
             }
-        }
-        if (part == 0)
-            for (int i = threadIdx.x; i < a.scales; i += NT) {
-                const float s = a.x_scale[token * a.scales + i];
-                for (int j = 0; j < a.topk; ++j)
-                    if (pos[j] >= 0) a.row_scales[int64_t(pos[j]) * a.scales + i] = s;
-            }
-    } else {
-        uint2 q[CH];
-        float s[CH];
+        n[i] += before[i];
+    }
+    int at = scan_start(n, s_scan);                        // (a barrier behind every read of count)
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        if (blockIdx.x == 0 && e <= a.E) a.offsets[e] = at;
+        if (e < a.E) count[e] = at + before[i];
+        at += n[i];
+    }
+    if (blockIdx.x == 0 && a.E == kMaxE && threadIdx.x == kThreads - 1) a.offsets[kMaxE] = at;
+    __syncthreads();
+    if (wv == 0) place_slots(a, own, last * a.topk, count, pos);
+    __syncthreads();
+    const bool whole = u1 - u0 <= 64 * CH;                 // the part in the wave's registers
+    for (int t = first + wv; t < last; t += kWaves) {
+        bool loaded = t < first + kWaves;
+        uint32_t bits = 0;
         if constexpr (kMode == kSortInt8) {
+            for (int u = u0; u < u1; u += 64 * CH) {
+                if (!loaded) load(t, u);
 #pragma unroll
-            for (int i = 0; i < NT / 64; ++i) bits = max(bits, s_max[i]);
-            float inverse;
-            s[0] = int8_scale(bits, inverse);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) q[c] = int8_codes(v[c], inverse);
-        } else {
-#pragma unroll
-            for (int c = 0; c < CH; ++c) s[c] = quant8<16>(v[c], q[c].x, q[c].y);   // parts are whole groups
-        }
-        for (int j = 0; j < a.topk; ++j) {
-            const int p = __builtin_amdgcn_readfirstlane(pos[j]);
-            if (p < 0) continue;
-            uint8_t* to = a.rows + int64_t(p) * a.cols;
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int u = u0 + c * NT;
-                if (u < u1) {
-                    *reinterpret_cast<uint2*>(to + int64_t(u) * 8) = q[c];
-                    if (kMode == kSortFp8 && (threadIdx.x & 15) == 0)
-                        a.row_scales[int64_t(p) * a.scales + (u >> 4)] = s[c];
-                }
+                for (int c = 0; c < CH; ++c)
+                    bits = pk_max_u16(bits, pk_max_u16(abs_max8(p[c].v[0]), abs_max8(p[c].v[1])));
+                loaded = whole;
             }
-            if (kMode == kSortInt8 && threadIdx.x == 0) a.row_scales[p] = s[0];
+            bits = wave_max_u16(bits);
         }
+        const int* mine = pos + (t - first) * a.topk;
+        for (int u = u0; u < u1; u += 64 * CH) {
+            if (!loaded) load(t, u);
+            store_pieces<kMode, CH>(a, p, mine, u + lane, u1, 64, bits);
+            loaded = false;
+        }
+        if (kMode == kSortCopy && u0 == 0) copy_scales(a, t, mine, lane, 64);
     }
 }
 
+template <SortMode kMode>
+hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
+    const int per = batch_tokens(a.T);
+    constexpr int kSpan = 1024;                            // pieces of a part
+    const int span = kMode == kSortInt8 ? a.units : kSpan;
+    int rep = 0;
+    while (rep < 3 && (2 * a.E << (rep + 1)) <= 2 * kMaxE) ++rep;
+    void (*kern)(SortArgs, int, int, int) = a.units <= 64    ? sort_batch_kernel<kMode, 1>
+                                       : a.units <= 128 ? sort_batch_kernel<kMode, 2>
+                                       : a.units <= 256 ? sort_batch_kernel<kMode, 4>
+                                       : a.units <= 512 || kMode != kSortCopy ? sort_batch_kernel<kMode, 8>
+                                                                              : sort_batch_kernel<kMode, 16>;
+    const dim3 grid((a.T + per - 1) / per, (a.units + span - 1) / span);
+    return start(kern, grid, kThreads, s, a, per, rep, span);
+}
+
+// Whether few ids are read so few times that every workgroup may compare them all
+// (sort_move_kernel<.., true>): ids read in all, us in that form / in the batch
+// form: 512 tokens of 4096 to 8 experts, to int8 (2.1 M) 8.7 / 9.9, 300 of 7168
+// in four parts (2.9 M) 11.5 / 12.9, 512 of 7168 (8.4 M) 17.5 / 15.7, 1031 of
+// 4096 to int8 (8.5 M) 19.3 / 14.5.  Few tokens do not fill the batch form's waves.
+bool few_ids(const SortArgs& a, int parts) { return a.T <= 256 || int64_t(a.T) * parts * a.R <= 4 << 20; }
+
 template <SortMode kMode, int NT, int CH>
-hipError_t launch_move(const SortArgs& a, bool one, hipStream_t s) {
+hipError_t launch_move(const SortArgs& a, bool counted, hipStream_t s) {
     // parts of at most NT * CH pieces, of equal length but for the rounding to whole groups
     const int parts = kMode == kSortInt8 ? 1 : (a.units + NT * CH - 1) / (NT * CH);
-    const int span = kMode == kSortInt8 ? a.units : ((a.units + parts - 1) / parts + 15) / 16 * 16;
-    const int64_t n = int64_t(a.T) * parts + (one ? 1 : 0);
+    const int span = kMode == kSortInt8 ? a.units : ((a.units + parts - 1) / parts + 7) / 8 * 8;
+    if (!counted && !few_ids(a, parts)) return launch_batch<kMode>(a, s);
+    const int64_t n = int64_t(a.T) * parts + (counted ? 0 : 1);
     void (*kern)(SortArgs, int, int) =
-        one ? sort_move_kernel<kMode, NT, CH, true> : sort_move_kernel<kMode, NT, CH, false>;
+        counted ? sort_move_kernel<kMode, NT, CH, false> : sort_move_kernel<kMode, NT, CH, true>;
     return start(kern, grid_of(n), NT, s, a, parts, span);
 }
 
-hipError_t launch_move(const SortArgs& a, SortMode mode, bool one, hipStream_t s) {
-    if (mode == kSortCopy) return launch_move<kSortCopy, 256, 1>(a, one, s);
-    if (mode == kSortFp8) return launch_move<kSortFp8, 256, 1>(a, one, s);
-    if (a.units <= 256) return launch_move<kSortInt8, 256, 1>(a, one, s);
-    if (a.units <= 512) return launch_move<kSortInt8, 256, 2>(a, one, s);
-    if (a.units <= 1024) return launch_move<kSortInt8, 256, 4>(a, one, s);
-    if (a.units <= 2048) return launch_move<kSortInt8, 1024, 2>(a, one, s);
-    static_assert(MOE_MAX_INT8_K <= 1024 * 4 * 8, "a row in one workgroup's registers");
-    return launch_move<kSortInt8, 1024, 4>(a, one, s);
+hipError_t launch_move(const SortArgs& a, SortMode mode, bool counted, hipStream_t s) {
+    if (mode == kSortCopy) return launch_move<kSortCopy, 256, 1>(a, counted, s);
+    if (mode == kSortFp8) return launch_move<kSortFp8, 256, 1>(a, counted, s);
+    if (a.units <= 256) return launch_move<kSortInt8, 256, 1>(a, counted, s);
+    if (a.units <= 512) return launch_move<kSortInt8, 256, 2>(a, counted, s);
+    if (a.units <= 1024) return launch_move<kSortInt8, 256, 4>(a, counted, s);
+    static_assert(MOE_MAX_INT8_K <= 1024 * 2 * 16, "a row in one workgroup's registers");
+    return launch_move<kSortInt8, 1024, 2>(a, counted, s);
 }
 
 }  // namespace
 
-SortPlan plan_sort(int64_t R, int E) {
-    (void)E;
-    if (R <= kOneLaunchSlots) return {0, 0};
+SortPlan plan_sort(int64_t R) {
+    if (R <= kBatchMostSlots) return {0, 0};
     // 1024 slots a block, more where there would be over kMostBlocks of them (a
     // block reads the counts of all)
     const int64_t slots = std::max<int64_t>(1024, (R + kMostBlocks - 1) / kMostBlocks + 255) / 256 * 256;
@@ -319,11 +480,11 @@ SortPlan plan_sort(int64_t R, int E) {
 }
 
 hipError_t launch_sort_rows(const SortArgs& a, SortMode mode, hipStream_t s) {
-    const SortPlan p = plan_sort(a.R, a.E);
-    if (p.blocks == 0) return launch_move(a, mode, true, s);
+    const SortPlan p = plan_sort(a.R);
+    if (p.blocks == 0) return launch_move(a, mode, false, s);
     hipError_t e = start(sort_count_kernel, dim3(p.blocks), kThreads, s, a, p.slots);
     if (e == hipSuccess) e = start(sort_place_kernel, dim3(p.blocks), kThreads, s, a, p.slots, p.blocks);
-    return e == hipSuccess ? launch_move(a, mode, false, s) : e;
+    return e == hipSuccess ? launch_move(a, mode, true, s) : e;
 }
 
 }  // namespace moe

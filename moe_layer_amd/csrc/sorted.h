@@ -24,7 +24,7 @@ struct SortArgs {
     int32_t* counts;           // scratch [blocks, E]
     int T, topk, E, R;         // R = T * topk
     int cols;
-    int units;                 // 16-byte pieces of a source row
+    int units;                 // 16-byte pieces of a row of `rows`
     int scales;                // scales of a row that is copied or made
 };
 // slots per block of the counted form, and its blocks; 0 blocks where the
@@ -32,7 +32,7 @@ struct SortArgs {
 struct SortPlan {
     int slots, blocks;
 };
-SortPlan plan_sort(int64_t R, int E);
+SortPlan plan_sort(int64_t R);
 hipError_t launch_sort_rows(const SortArgs& a, SortMode mode, hipStream_t s);
 
 struct CombineArgs {
@@ -99,6 +99,24 @@ __device__ __forceinline__ uint2 int8_codes(const i32x4& w, float inverse) {
         pair[q] = __builtin_amdgcn_perm(__float_as_uint(__builtin_fmaf(bf16_hi(w[q]), inverse, kWhole)),
                                         __float_as_uint(__builtin_fmaf(bf16_lo(w[q]), inverse, kWhole)), 0x0c0c0400u);
     return uint2{pair[0] | pair[1] << 16, pair[2] | pair[3] << 16};
+}
+
+// fp8 codes (moe_quant_act's rule) of 16 columns by each of 8 neighbouring lanes,
+// which hold a 128-column group; returns the scale
+__device__ __forceinline__ float quant16(const i32x4& a, const i32x4& b, i32x4& codes) {
+    uint32_t m = pk_max_u16(abs_max8(a), abs_max8(b));
+    m = dpp_max_u16<0xb1>(m);                              // quad_perm [1,0,3,2]
+    m = dpp_max_u16<0x4e>(m);                              // quad_perm [2,3,0,1]
+    m = dpp_max_u16<0x141>(m);                             // row_half_mirror
+    const float s = fp8_group_scale(__uint_as_float(max(m & 0xffffu, m >> 16) << 16));
+    const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));   // 1 / s, as in quant8
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t w0 = uint32_t(q < 2 ? a[2 * q] : b[2 * q - 4]), w1 = uint32_t(q < 2 ? a[2 * q + 1] : b[2 * q - 3]);
+        codes[q] = int(pack_e4m3(__fmul_rn(bf16_lo(w0), inv), __fmul_rn(bf16_hi(w0), inv), __fmul_rn(bf16_lo(w1), inv),
+                                 __fmul_rn(bf16_hi(w1), inv)));
+    }
+    return s;
 }
 
 }  // namespace

@@ -68,7 +68,7 @@ MOE_API int64_t moe_sort_scratch_bytes(int32_t T, int32_t topk, int32_t E) {
     if (bad_routing(T, topk) || E < 1 || E > MOE_MAX_EXPERTS) return MOE_ERR_INVALID_ARG;
     const int64_t R = int64_t(T) * topk;
     if (R > kMaxRows) return MOE_ERR_UNSUPPORTED;
-    return int64_t(plan_sort(R, E).blocks) * E * 4;
+    return int64_t(plan_sort(R).blocks) * E * 4;
 }
 
 MOE_API int moe_sort_rows(const void* x, const float* x_scale, const int32_t* topk_ids, int32_t T, int32_t topk,
@@ -111,7 +111,7 @@ MOE_API int moe_sort_rows(const void* x, const float* x_scale, const int32_t* to
     a.E = E;
     a.R = int(R);
     a.cols = cols;
-    a.units = int(xb / 16);
+    a.units = int(rb / 16);
     a.scales = rs;
     const SortMode mode = xtype == rowtype ? kSortCopy : to_int8 ? kSortInt8 : kSortFp8;
     return hip_status(launch_sort_rows(a, mode, stream));

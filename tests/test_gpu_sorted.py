@@ -126,6 +126,37 @@ def test_sort_rows_int8_of_every_row_size(cols):
     check_sort(5, 3, 4, cols, "bf16", "int8", routing(rng, 5, 3, 4), cols)
 
 
+@pytest.mark.parametrize("kind,quant", KINDS)
+@pytest.mark.parametrize("cols", [8448, 16640, 24576])
+def test_sort_rows_long_rows_of_many_tokens(cols, kind, quant):
+    """Rows longer than a wave holds, in a batch of more tokens than workgroups compare ids for."""
+    rng = np.random.default_rng(cols)
+    check_sort(1100, 4, 9, cols, kind, quant, routing(rng, 1100, 4, 9, away=0.3), cols)
+
+
+@pytest.mark.parametrize("T,k", [(1448, 1), (1449, 1), (511, 8), (513, 8), (724, 4), (725, 4), (2051, 8), (4095, 7)])
+def test_sort_rows_between_the_forms(T, k):
+    """Batches around the size from which tokens share a workgroup, and of several tokens a wave."""
+    rng = np.random.default_rng(T)
+    check_sort(T, k, 33, 64, "bf16", "int8", routing(rng, T, k, 33, away=0.1), T)
+
+
+def test_sort_rows_ids_anywhere():
+    """Ids that start at every 4-byte place of a 16-byte piece."""
+    rng, d = np.random.default_rng(8), dev()
+    for T, k in ((3, 3), (700, 5)):
+        ids = routing(rng, T, k, 12, away=0.2)
+        want_off, want_inv, _ = O.sort_slots(ids, 12)
+        x = torch.randn(T, 64, device=d).bfloat16()
+        for at in range(4):
+            buf = torch.full((T * k + 8,), 5, dtype=torch.int32, device=d)
+            view = buf[at: at + T * k].view(T, k)
+            view.copy_(torch.from_numpy(ids))
+            _, _, off, inv = ops.moe_sort_rows(x, view, 12)
+            np.testing.assert_array_equal(off.cpu().numpy(), want_off)
+            np.testing.assert_array_equal(inv.cpu().numpy(), want_inv)
+
+
 def test_sort_rows_sizes_around_the_forms():
     """Slots on both sides of where the counted form begins, and of its blocks."""
     rng = np.random.default_rng(17)
