@@ -329,13 +329,177 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     }
 }
 
+// One 256 x 256 tile of int8 operands.  Where all waves read a stage first and
+// multiply then, the matrix cores idle for a third of it, so the waves run in two
+// groups, one wave of each to a SIMD: while one group reads the operands of 64 bytes
+// of K, the other multiplies.  A barrier every half stage keeps them apart; the ring
+// needs every second one.  Loads go out in the reading part: in the multiplying one
+// each waits for the others' and the products for it (224 against 183 us).
+//
+// LDS holds five units of 256 rows x 128 bytes, weights and tokens of a stage in
+// turn, so the next stage's tokens and the weights of the one after are on their way
+// while a stage is read: unit n goes where unit n - 5 was.
+//
+// 8192 x 4096 x 7168, operands random over all codes: 178 us, 2.70 POP/s (a library
+// product 195 us; this tile with all waves in step 204).  What bounds it is power: the
+// same product of zeros takes 137 us, 3.52 POP/s, at the rate of the matrix
+// instructions alone.  Four waves of 128 x 128 outputs, which read a third less from
+// LDS, took 182, and longer for short K.
+template <bool NTW>
+__device__ __forceinline__ void tile_product_int8(const RowsGemmArgs& g, lds_t* lds, int e, int row0, int row1,
+                                                  int n0) {
+    constexpr int SA = 8, SB = 4, kUnit = 256 * 128, kCols = 128;
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wv & 1, wt = wv >> 1, group = wv >> 2;
+    const int lr = lane & 15, lk = lane >> 4;
+    const int64_t kbytes = g.K;
+    const int steps = int((kbytes + 127) >> 7);
+    const int part = (kbytes & 127) ? steps - 1 : -1;        // the step that is a part of one
+    const bool past = (((lane & 7) ^ (lane >> 3)) << 4) >= int(kbytes & 127);
+
+    const uint8_t* wbase = g.w + (int64_t(e) * g.N + n0) * kbytes;
+    const uint8_t* abase = g.a + int64_t(row0) * kbytes;
+    uint32_t woff[4], aoff[4];                               // this lane's bytes of each piece
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = 8 * (wv + 8 * j) + (lane >> 3);
+        const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) << 4;
+        woff[j] = uint32_t(min(r, g.N - 1 - n0)) * uint32_t(kbytes) + chunk;
+        aoff[j] = uint32_t(min(r, row1 - 1 - row0)) * uint32_t(kbytes) + chunk;
+    }
+    // piece j of stage st's weights or tokens (the latter are as many of them)
+    auto load = [&](bool weights, int st, int unit, int j) {
+        const uint8_t* from = (weights ? wbase : abase) + (int64_t(st) << 7) + (weights ? woff[j] : aoff[j]);
+        if (st == part && past) from = kNoChunk;
+        lds_t* const to = lds + unit * kUnit + (wv + 8 * j) * 1024;
+        if (NTW && weights) load_piece<true>(from, to, true);
+        else load_piece<false>(from, to, weights);
+    };
+    auto issue = [&](bool weights, int st, int unit) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load(weights, st, unit, j);
+    };
+    auto wrap = [](int unit) { return unit >= 5 ? unit - 5 : unit; };
+    const float *a_scale = g.a_scale, *w_scale = g.w_scale;
+    // the tile's scales, weight rows first
+    auto issue_scales = [&](int unit) {
+        const float* from = wv < 4 ? w_scale + int64_t(e) * g.N + min(n0 + 64 * wv + lane, g.N - 1)
+                                   : a_scale + min(row0 + 64 * (wv - 4) + lane, row1 - 1);
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(from), lds + unit * kUnit + 256 * wv, 4, 0, 0);
+    };
+    // stage st has landed (st == steps: the scales): only what went after its tokens may not have
+    auto wait_stage = [&](int st) {
+        if (st + 1 < steps) wait_vm<4>();
+        else wait_vm<0>();
+    };
+
+    i32x4 acc[SA][SB];
+#pragma unroll
+    for (int i = 0; i < SA; ++i)
+#pragma unroll
+        for (int t = 0; t < SB; ++t) acc[i][t] = i32x4{0, 0, 0, 0};
+    const uint32_t arow = uint32_t(wm * kCols + lr) * 128, brow = uint32_t(wt * 64 + lr) * 128;
+    const uint32_t c0 = uint32_t(lk ^ (lr & 7)) << 4;
+    // a wave whose tokens or weight rows all lie past the end only loads
+    const bool idle = wt * 64 >= row1 - row0 || n0 + wm * kCols >= g.N;
+    i32x4 a[SA], b[SB];
+    auto read = [&](int iw, uint32_t half) {
+        if (idle) return;
+        const lds_t* const from = lds + iw * kUnit + arow + (c0 ^ half);
+        const lds_t* const tokens = lds + wrap(iw + 1) * kUnit + brow + (c0 ^ half);
+#pragma unroll
+        for (int t = 0; t < SB; ++t) b[t] = *reinterpret_cast<lds_v4*>(tokens + t * 2048);
+#pragma unroll
+        for (int i = 0; i < SA; ++i) a[i] = *reinterpret_cast<lds_v4*>(from + i * 2048);
+    };
+    auto multiply = [&]() {
+        if (idle) return;
+#pragma unroll
+        for (int i = 0; i < SA; ++i)
+#pragma unroll
+            for (int t = 0; t < SB; ++t) acc[i][t] = mma(a[i], b[t], acc[i][t]);
+    };
+
+    issue(true, 0, 0);
+    issue(false, 0, 1);
+    if (steps > 1) issue(true, 1, 2);
+    wait_stage(0);
+    barrier();
+    int iw = 0;                                              // the unit of the stage's weights
+    auto first = [&](int st, int w) {                        // 64 bytes of K, and the next stage's tokens on their way
+        read(w, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (st + 1 < steps) issue(false, st + 1, wrap(w + 3));
+        else issue_scales(wrap(w + 3));
+        wait_lgkm0();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto second = [&](int st, int w) {                       // the other 64, and the weights of the stage after that
+        read(w, 64);
+        __builtin_amdgcn_sched_barrier(0);
+        if (st + 2 < steps) issue(true, st + 2, wrap(w + 4));
+        wait_lgkm0();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (group == 0) {
+        for (int st = 0; st < steps; ++st) {
+            first(st, iw);
+            multiply();
+            barrier();
+            second(st, iw);
+            multiply();
+            wait_stage(st + 1);
+            barrier();
+            iw = wrap(iw + 2);
+        }
+    } else {
+        for (int st = 0; st < steps; ++st) {
+            if (st > 0) multiply();
+            first(st, iw);
+            barrier();
+            multiply();
+            second(st, iw);
+            wait_stage(st + 1);
+            barrier();
+            iw = wrap(iw + 2);
+        }
+        multiply();
+    }
+    f32x4 sw[SA];
+    float sa[SB];
+    {
+        typedef const __attribute__((address_space(3))) f32x4 lds_f4;
+        const lds_t* const scales = lds + wrap(iw + 1) * kUnit;
+#pragma unroll
+        for (int i = 0; i < SA; ++i) sw[i] = *reinterpret_cast<lds_f4*>(scales + 4 * (wm * kCols + 16 * i + 4 * lk));
+#pragma unroll
+        for (int t = 0; t < SB; ++t) sa[t] = *reinterpret_cast<lds_f*>(scales + 1024 + 4 * (wt * 64 + 16 * t + lr));
+    }
+    __syncthreads();
+    lds_t* const rows16 = lds + wv * (16 * kOutRow<kCols>);
+#pragma unroll
+    for (int t = 0; t < SB; ++t) {
+#pragma unroll
+        for (int i = 0; i < SA; ++i)
+            stage4<kCols>(rows16, lr, 16 * i + 4 * lk, scaled(acc[i][t], sa[t], sw[i]));
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        store_tile<kCols, 16, 64, true>(g, rows16, row0 + wt * 64 + 16 * t, row1, n0 + wm * kCols);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 template <RowsKind KIND, int BW, int BT, int WW, int WT, int S, bool NTW>
 __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g, int ntiles, int band) {
     // The last block of a group, of half the rows or fewer: the room of the
     // missing ones goes into a third slot and all waves share the rest (20000
     // rows in 64 bf16 groups of 2000 x 1024 120 -> 115 us).
     constexpr bool kPart64 = BW == 256, kPart128 = BW == 256 && BT == 256;
-    constexpr int kLds = std::max({tile_lds<KIND, BW, BT, S>(), kPart64 ? tile_lds<KIND, BW, 64, 3>() : 0,
+    constexpr bool kGroups = KIND == kRowsInt8 && kPart128;
+    constexpr int kLds = std::max({kGroups ? 5 * 32768 : tile_lds<KIND, BW, BT, S>(),
+                                   kPart64 ? tile_lds<KIND, BW, 64, 3>() : 0,
                                    kPart128 ? tile_lds<KIND, BW, 128, 3>() : 0});
     // one LDS object: with several, the compiler waits for every direct-to-LDS
     // load before each LDS read
@@ -362,7 +526,8 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
     if constexpr (kPart128) {
         if (row1 - row0 <= 128) return tile_product<KIND, BW, 128, 4, 2, 3, NTW>(g, ring, e, row0, row1, n0);
     }
-    tile_product<KIND, BW, BT, WW, WT, S, NTW>(g, ring, e, row0, row1, n0);
+    if constexpr (kGroups) tile_product_int8<NTW>(g, ring, e, row0, row1, n0);
+    else tile_product<KIND, BW, BT, WW, WT, S, NTW>(g, ring, e, row0, row1, n0);
 }
 
 template <RowsKind KIND, int BW, int BT, int WW, int WT, int S>
