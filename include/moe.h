@@ -570,7 +570,8 @@ MOE_API int moe_grouped_gemm(const void* a, const float* a_scale, const void* w,
 /* Which kernel moe_gemm_fp8, moe_gemm_int8 or moe_grouped_gemm takes for these sizes, reported
  * like moe_plan_info so that a test can check it without timing. */
 typedef struct moe_gemm_plan_info {
-    int32_t split;       /* 1: K split over a workgroup's waves; 0: tiles shared in LDS */
+    int32_t split;       /* 1: K split over a workgroup's waves; 0: tiles shared in LDS;
+                            2: the same, two workgroups a CU (INT8 only) */
     int32_t block_cols;  /* outputs of a row per workgroup */
     int32_t block_rows;  /* rows of a group per workgroup */
     int32_t one_pass;    /* 1: the weights are loaded past the caches' replacement */

@@ -126,7 +126,7 @@ hipError_t launch_rows_gemm(const RowsGemmArgs& g, RowsKind kind, hipStream_t s)
 // they are there.
 struct RowsPlan {
     bool split;
-    int shape, bw, bt;
+    int shape, bw, bt, per_cu;
     bool one_pass;
 };
 RowsPlan plan_rows_gemm(const RowsGemmArgs& g, RowsKind kind);

@@ -135,31 +135,37 @@ __device__ __forceinline__ void stage4(lds_t* tile, int t, int n, const f32x4& v
         i32x2{int(pack_bf16(v[0], v[1])), int(pack_bf16(v[2], v[3]))};
 }
 
-// V outputs per lane, V * 2 bytes aligned in every row (N % V == 0), by THREADS
-// neighbouring lanes.  NT: past the caches' replacement (tile_product).
-template <int BW, int BT, int THREADS, bool NT, int V, typename T>
-__device__ __forceinline__ void store_rows(const RowsGemmArgs& g, const lds_t* tile, int row0, int row1, int n0) {
-    typedef const __attribute__((address_space(3))) T lds_T;
-    constexpr int kPer = BW / V, kTurns = (BT * kPer + THREADS - 1) / THREADS;
+// Eight outputs per lane by THREADS neighbouring lanes, 16 bytes a store wherever a
+// row starts (global stores take any alignment; 6565 x 5413 x 496 int8 54.7 -> 45.2 us
+// against 2 bytes a store where N is odd), the last N % 8 of a row one by one.  NT:
+// past the caches' replacement (tile_product), but for long outputs whose rows are no
+// whole lines: the two halves of a line that tiles share should meet in L2 (us past it
+// / not: 8140 x 3448 x 1152, 56 MB, 44.2 / 38.3, 6565 x 5413 x 496, 71 MB, 52.1 /
+// 44.1; 5009 x 1642 x 592, 16 MB, 15.3 / 16.8, 3937 rows in 100 groups of 3368 x 384,
+// 27 MB, 34.4 / 36.4).
+template <int BW, int BT, int THREADS, bool NT>
+__device__ __forceinline__ void store_tile(const RowsGemmArgs& g, const lds_t* tile, int row0, int row1, int n0) {
+    typedef __attribute__((ext_vector_type(4), aligned(2))) int anywhere_v4;
+    typedef const __attribute__((address_space(3))) uint16_t lds_u16;
+    constexpr int kPer = BW / 8, kTurns = (BT * kPer + THREADS - 1) / THREADS;
     const int live = min(BT, row1 - row0);
+    const bool past = NT && ((g.N & 63) == 0 || int64_t(g.rows) * g.N < 16 << 20);
     // several pieces read ahead of their stores
 #pragma unroll(kTurns < 8 ? kTurns : 4)
     for (int q = 0; q < kTurns; ++q) {
         const int i = threadIdx.x % THREADS + q * THREADS;
-        const int r = i / kPer, c = (i % kPer) * V;
-        if (r < live && n0 + c < g.N) {
-            const T v = *reinterpret_cast<lds_T*>(tile + r * kOutRow<BW> + 2 * c);
-            T* const to = reinterpret_cast<T*>(g.out + int64_t(row0 + r) * g.N + n0 + c);
-            if constexpr (NT) __builtin_nontemporal_store(v, to);
-            else *to = v;
+        const int r = i / kPer, c = (i % kPer) * 8;
+        if (r >= live || n0 + c >= g.N) continue;
+        const lds_t* const from = tile + r * kOutRow<BW> + 2 * c;
+        uint16_t* const to = g.out + int64_t(row0 + r) * g.N + n0 + c;
+        if (n0 + c + 8 <= g.N) {
+            const i32x4 v = *reinterpret_cast<lds_v4*>(from);
+            if (past) __builtin_nontemporal_store(v, reinterpret_cast<anywhere_v4*>(to));
+            else *reinterpret_cast<anywhere_v4*>(to) = v;
+        } else {
+            for (int k = 0; n0 + c + k < g.N; ++k) to[k] = *reinterpret_cast<lds_u16*>(from + 2 * k);
         }
     }
-}
-template <int BW, int BT, int THREADS, bool NT>
-__device__ __forceinline__ void store_tile(const RowsGemmArgs& g, const lds_t* tile, int row0, int row1, int n0) {
-    if ((g.N & 7) == 0) store_rows<BW, BT, THREADS, NT, 8, i32x4>(g, tile, row0, row1, n0);
-    else if ((g.N & 1) == 0) store_rows<BW, BT, THREADS, NT, 2, uint32_t>(g, tile, row0, row1, n0);
-    else store_rows<BW, BT, THREADS, NT, 1, uint16_t>(g, tile, row0, row1, n0);
 }
 
 // One operand of a 16-row subtile for a 128-byte step of K, from this lane's two

@@ -491,6 +491,164 @@ __device__ __forceinline__ void tile_product_int8(const RowsGemmArgs& g, lds_t* 
     }
 }
 
+// A tile of 256 x BT int8 outputs by four waves in half of a CU's LDS, so that two
+// workgroups share a CU and one multiplies while the other reads, starts or stores.
+// Where K is short, starting and storing are a third of the tile above.
+//
+// The weights have two slots of 32 KB, the tokens one: every wave takes its tokens of
+// a whole stage into registers, and behind the barrier that says so the next ones go
+// where they were.
+constexpr int kPairLds = 80 * 1024;
+template <int BT, int WW, int WT, bool NTW>
+__device__ __forceinline__ void tile_product_pair(const RowsGemmArgs& g, lds_t* lds, int e, int row0, int row1, int n0) {
+    constexpr int BW = 256, SA = BW / WW / 16, SB = BT / WT / 16, kCols = BW / WW;
+    constexpr int kW = BW * 128;                             // bytes of a stage's weights
+    constexpr int PW = BW / 8 / 4, PT = BT / 8 / 4;          // loads of a wave
+    static_assert(WW * WT == 4 && 2 * kW + BT * 128 <= kPairLds, "LDS");
+    lds_t* const tslot = lds + 2 * kW;
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wv % WW, wt = wv / WW;
+    const int lr = lane & 15, lk = lane >> 4;
+    const int64_t kbytes = g.K;
+    const int steps = int((kbytes + 127) >> 7);
+    const int part = (kbytes & 127) ? steps - 1 : -1;        // the step that is a part of one
+    const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) << 4;
+    const bool past = int(chunk) >= int(kbytes & 127);
+
+    const uint8_t* wbase = g.w + (int64_t(e) * g.N + n0) * kbytes;
+    const uint8_t* abase = g.a + int64_t(row0) * kbytes;
+    uint32_t woff[PW], toff[PT];                             // this lane's bytes of each piece
+#pragma unroll
+    for (int j = 0; j < PW; ++j)
+        woff[j] = uint32_t(min(8 * (wv + 4 * j) + (lane >> 3), g.N - 1 - n0)) * uint32_t(kbytes) + chunk;
+#pragma unroll
+    for (int j = 0; j < PT; ++j)
+        toff[j] = uint32_t(min(8 * (wv + 4 * j) + (lane >> 3), row1 - 1 - row0)) * uint32_t(kbytes) + chunk;
+    auto issue_weights = [&](int st) {
+#pragma unroll
+        for (int j = 0; j < PW; ++j) {
+            const uint8_t* from = wbase + woff[j] + (int64_t(st) << 7);
+            if (st == part && past) from = kNoChunk;
+            load_piece<NTW>(from, lds + (st & 1) * kW + (wv + 4 * j) * 1024, true);
+        }
+    };
+    auto issue_tokens = [&](int st) {
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+            const uint8_t* from = abase + toff[j] + (int64_t(st) << 7);
+            if (st == part && past) from = kNoChunk;
+            load_piece<NTW>(from, tslot + (wv + 4 * j) * 1024, false);
+        }
+    };
+    // the tile's scales, weight rows first, in the tokens' slot
+    const float *a_scale = g.a_scale, *w_scale = g.w_scale;
+    auto issue_scales = [&]() {
+#pragma unroll
+        for (int p = 0; p < (BW + BT + 255) / 256; ++p) {
+            const int i = 256 * p + 64 * wv + lane;
+            if (256 * p + 64 * wv >= BW + BT) break;
+            const float* from = i < BW ? w_scale + int64_t(e) * g.N + min(n0 + i, g.N - 1)
+                                       : a_scale + min(row0 + i - BW, row1 - 1);
+            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(from), tslot + 1024 * p + 256 * wv, 4, 0, 0);
+        }
+    };
+
+    i32x4 acc[SA][SB];
+#pragma unroll
+    for (int i = 0; i < SA; ++i)
+#pragma unroll
+        for (int t = 0; t < SB; ++t) acc[i][t] = i32x4{0, 0, 0, 0};
+    const uint32_t arow = uint32_t(wm * kCols + lr) * 128, brow = uint32_t(wt * (BT / WT) + lr) * 128;
+    const uint32_t c0 = uint32_t(lk ^ (lr & 7)) << 4;
+    // a wave whose tokens or weight rows all lie past the end only loads
+    const bool idle = wt * (BT / WT) >= row1 - row0 || n0 + wm * kCols >= g.N;
+    i32x4 a[SA], b[2][SB];
+    auto read = [&](int st, int h) {
+        const lds_t* const from = lds + (st & 1) * kW + arow + (c0 ^ (64 * h));
+#pragma unroll
+        for (int i = 0; i < SA; ++i) a[i] = *reinterpret_cast<lds_v4*>(from + i * 2048);
+    };
+    auto multiply = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < SA; ++i)
+#pragma unroll
+            for (int t = 0; t < SB; ++t) acc[i][t] = mma(a[i], b[h][t], acc[i][t]);
+    };
+
+    issue_weights(0);
+    issue_tokens(0);
+    for (int st = 0; st < steps; ++st) {
+        wait_vm<0>();                                        // stage st, sent a stage ago
+        barrier();
+        if (!idle) {
+#pragma unroll
+            for (int t = 0; t < SB; ++t) {
+                b[0][t] = *reinterpret_cast<lds_v4*>(tslot + brow + c0 + t * 2048);
+                b[1][t] = *reinterpret_cast<lds_v4*>(tslot + brow + (c0 ^ 64) + t * 2048);
+            }
+            read(st, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (st + 1 < steps) issue_weights(st + 1);           // where the stage before's were
+        wait_lgkm0();
+        barrier();                                           // the tokens are in registers
+        if (st + 1 < steps) issue_tokens(st + 1);
+        else issue_scales();
+        __builtin_amdgcn_sched_barrier(0);
+        if (!idle) {
+            multiply(0);
+            read(st, 1);
+            multiply(1);
+        }
+    }
+    wait_vm<0>();
+    __syncthreads();                                         // the scales have landed, the weights are read
+    typedef const __attribute__((address_space(3))) f32x4 lds_f4;
+    f32x4 sw[SA];
+#pragma unroll
+    for (int i = 0; i < SA; ++i) sw[i] = *reinterpret_cast<lds_f4*>(tslot + 4 * (wm * kCols + 16 * i + 4 * lk));
+    lds_t* const rows16 = lds + wv * (16 * kOutRow<kCols>);  // in the weights' place
+    static_assert(4 * 16 * kOutRow<kCols> <= 2 * kW, "outputs");
+#pragma unroll
+    for (int t = 0; t < SB; ++t) {
+        const float sa = *reinterpret_cast<lds_f*>(tslot + 4 * (BW + wt * (BT / WT) + 16 * t + lr));
+#pragma unroll
+        for (int i = 0; i < SA; ++i) stage4<kCols>(rows16, lr, 16 * i + 4 * lk, scaled(acc[i][t], sa, sw[i]));
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        store_tile<kCols, 16, 64, true>(g, rows16, row0 + wt * (BT / WT) + 16 * t, row1, n0 + wm * kCols);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// item -> (band of weight tiles, row block, tile in the band): the items an XCD works
+// on at a time share `band` weight tiles and some row blocks.  False past the last.
+template <int BW, int BT>
+__device__ __forceinline__ bool find_tile(const RowsGemmArgs& g, int ntiles, int band, int& e, int& row0, int& row1,
+                                          int& n0) {
+    const int slots = count_blocks<BT>(g);
+    int64_t item;
+    if (!xcd_item(int64_t(slots) * ntiles, item)) return false;   // the whole workgroup alike
+    const int64_t per_band = int64_t(band) * slots;
+    const int b = int(item / per_band);
+    const int64_t in = item - b * per_band;
+    const int wide = min(band, ntiles - b * band);
+    const int slot = int(in / wide);
+    n0 = (b * band + int(in % wide)) * BW;
+    return find_block<BT>(g, slot, e, row0, row1);
+}
+
+template <bool NTW>
+__global__ __launch_bounds__(256, 2) void rows_pair_kernel(RowsGemmArgs g, int ntiles, int band) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kPairLds];
+    int e, row0, row1, n0;
+    if (!find_tile<256, 128>(g, ntiles, band, e, row0, row1, n0)) return;
+    if (row1 - row0 <= 64) tile_product_pair<64, 4, 1, NTW>(g, (lds_t*)lds, e, row0, row1, n0);
+    else tile_product_pair<128, 2, 2, NTW>(g, (lds_t*)lds, e, row0, row1, n0);
+}
+
 template <RowsKind KIND, int BW, int BT, int WW, int WT, int S, bool NTW>
 __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g, int ntiles, int band) {
     // The last block of a group, of half the rows or fewer: the room of the
@@ -507,18 +665,8 @@ __global__ __launch_bounds__(64 * WW * WT) void rows_tile_kernel(RowsGemmArgs g,
     static_assert(kLds <= 160 * 1024, "LDS");
     lds_t* const ring = (lds_t*)lds;
 
-    // item -> (band of weight tiles, row block, tile in the band): the items an
-    // XCD works on at a time share `band` weight tiles and some row blocks
-    const int slots = count_blocks<BT>(g);
-    int64_t item;
-    if (!xcd_item(int64_t(slots) * ntiles, item)) return;    // the whole workgroup alike
-    const int64_t per_band = int64_t(band) * slots;
-    const int b = int(item / per_band);
-    const int64_t in = item - b * per_band;
-    const int wide = min(band, ntiles - b * band);
-    const int slot = int(in / wide), n0 = (b * band + int(in % wide)) * BW;
-    int e, row0, row1;
-    if (!find_block<BT>(g, slot, e, row0, row1)) return;
+    int e, row0, row1, n0;
+    if (!find_tile<BW, BT>(g, ntiles, band, e, row0, row1, n0)) return;
 
     if constexpr (kPart64) {
         if (row1 - row0 <= 64) return tile_product<KIND, BW, 64, 4, 2, 3, NTW>(g, ring, e, row0, row1, n0);
@@ -550,6 +698,13 @@ hipError_t launch(const RowsGemmArgs& g, int shape, bool one_pass, hipStream_t s
     }
     if constexpr (KIND != kRowsFp8) {                        // of converted e4m3 operands: out of registers
         if (shape == 4) return launch_tile<KIND, 256, 256, 2, 4, 2>(g, one_pass, s);
+    }
+    if constexpr (KIND == kRowsInt8) {
+        if (shape == 5) {
+            const int ntiles = (g.N + 255) / 256;
+            void (*kern)(RowsGemmArgs, int, int) = one_pass ? rows_pair_kernel<true> : rows_pair_kernel<false>;
+            return start(kern, xcd_grid(block_slots(g, 128) * ntiles), 256, s, g, ntiles, std::min(kBand, ntiles));
+        }
     }
     return hipErrorInvalidValue;
 }

@@ -125,7 +125,7 @@ MOE_API int moe_gemm_plan(int32_t rows, int32_t E, int32_t N, int32_t K, int32_t
     g.N = N;
     g.K = K;
     const RowsPlan p = plan_rows_gemm(g, kind);
-    *out = moe_gemm_plan_info{p.split, p.bw, p.bt, p.one_pass};
+    *out = moe_gemm_plan_info{p.split ? 1 : p.per_cu == 2 ? 2 : 0, p.bw, p.bt, p.one_pass};
     return MOE_OK;
 }
 
