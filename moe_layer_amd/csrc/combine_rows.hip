@@ -164,9 +164,16 @@ hipError_t launch_bwd(const CombineArgs& a, hipStream_t s) {
     constexpr int NT = W <= 4 ? 256 : 64 * W, kTokens = NT / 64 / W;
     return start(combine_rows_bwd_kernel<W, kDots, kWeights>, grid_of((int64_t(a.T) + kTokens - 1) / kTokens), NT, s, a);
 }
+// Columns up to which a wave takes a token (us, one wave / four: 2048 tokens of 256
+// and 8 slots 5.7 / 9.1, of 512 7.1 / 10.0, of 1024 14.3 / 14.3, of 4096 48 / 47), and
+// tokens up to which sixteen waves do (four / sixteen: 64 x 7168 7.7 / 7.1, 200 x 7168
+// 10.7 / 9.6, 400 x 7168 17.6 / 18.7, 600 x 4096 15.3 / 19.1).
+constexpr int kWaveCols = 512, kFewTokens = 256;
+
 template <bool kDots, bool kWeights>
 hipError_t launch_bwd(const CombineArgs& a, hipStream_t s) {
-    if (a.T >= 2048 || a.cols <= 512) return launch_bwd<1, kDots, kWeights>(a, s);
+    if (a.cols <= kWaveCols) return launch_bwd<1, kDots, kWeights>(a, s);
+    if (a.T <= kFewTokens && a.cols > 2048) return launch_bwd<16, kDots, kWeights>(a, s);
     return launch_bwd<4, kDots, kWeights>(a, s);
 }
 
