@@ -49,7 +49,7 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lk = lane >> 4;
     const int64_t kbytes = int64_t(g.K) * (KIND == kRowsBf16 ? 2 : 1);
-    const int steps = int((kbytes + 127) >> 7);
+    const int steps = int((kbytes + (INT8 ? 127 : 0)) >> 7);
     const int n0 = tile * BW;
     lds_t* const ring = (lds_t*)lds + wv * D * kSlot;
 

@@ -75,7 +75,7 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     const int wm = wv % WW, wt = wv / WW;
     const int lr = lane & 15, lk = lane >> 4;
     const int64_t kbytes = int64_t(g.K) * (KIND == kRowsBf16 ? 2 : 1);
-    const int steps = int((kbytes + 127) >> 7);
+    const int steps = int((kbytes + (INT8 ? 127 : 0)) >> 7);
     const int part = INT8 && (kbytes & 127) ? steps - 1 : -1;   // the step that is a part of one
     const bool past = (((lane & 7) ^ (lane >> 3)) << 4) >= int(kbytes & 127);
 

@@ -21,7 +21,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kPlaceThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBatchMostSlots = 32768;
 constexpr int kMostBlocks = 256;
@@ -99,6 +99,16 @@ __device__ __forceinline__ void write_offsets(const SortArgs& a) {
     constexpr int kPer = kMaxE / NT;
     __shared__ int count[kMaxE];
     __shared__ int s_scan[NT / 64];
+    if (a.R <= 64) {
+        const int lane = threadIdx.x & 63;
+        const int id = lane < a.R ? a.ids[lane] : -1;
+        for (int e = threadIdx.x; e <= a.E; e += NT) {
+            int n = 0;
+            for (int i = 0; i < a.R; ++i) n += uint32_t(__builtin_amdgcn_readlane(id, i)) < uint32_t(e) ? 1 : 0;
+            a.offsets[e] = n;
+        }
+        return;
+    }
     for (int e = threadIdx.x; e < kMaxE; e += NT) count[e] = 0;
     __syncthreads();
     each_id<NT, 2>(a.ids, a.R, threadIdx.x, [&](int, int id) {
@@ -124,6 +134,15 @@ template <int NT>
 __device__ __forceinline__ void find_positions(const SortArgs& a, int t, int* pos) {
     constexpr int kAt = 8;
     const int lane = threadIdx.x & 63, own = t * a.topk;
+    if (a.R <= 64) {                                       // an id a lane: every wave by itself
+        const int id = lane < a.R ? a.ids[lane] : -1;
+        for (int j = 0; j < a.topk; ++j) {
+            const uint32_t e = uint32_t(__builtin_amdgcn_readlane(id, own + j));
+            const int n = __popcll(__ballot(uint32_t(id) < e + (lane < own + j ? 1u : 0u)));
+            if (lane == j) pos[j] = e < uint32_t(a.E) ? n : -1;
+        }
+        return;
+    }
     for (int j0 = 0; j0 < a.topk; j0 += kAt) {
         uint32_t e[kAt];
         int n[kAt];
@@ -146,15 +165,15 @@ __device__ __forceinline__ void find_positions(const SortArgs& a, int t, int* po
     }
 }
 
-// inv of slots first .. last - 1 by one wave, given each expert's next position;
-// also into pos[0 ..] where that is not null
-__device__ __forceinline__ void place_slots(const SortArgs& a, int first, int last, int* next, int* pos) {
+// inv of slots first .. last - 1 by one wave, given each expert's next position and
+// the ids of the first 64 slots; also into pos[0 ..] where that is not null
+__device__ __forceinline__ void place_slots(const SortArgs& a, int first, int last, int e, int* next, int* pos) {
     const int lane = threadIdx.x & 63;
     const uint64_t lower = (uint64_t(1) << lane) - 1;
     const int bits = a.E > 1 ? 32 - __clz(a.E - 1) : 0;
     for (int i = first; i < last; i += 64) {
         const int f = i + lane;
-        const int e = f < last ? a.ids[f] : -1;
+        if (i > first) e = f < last ? a.ids[f] : -1;
         const bool routed = uint32_t(e) < uint32_t(a.E);
         const uint64_t same = peers(e, routed, bits);
         int at = -1;
@@ -188,16 +207,16 @@ __global__ __launch_bounds__(kThreads) void sort_count_kernel(SortArgs a, int sl
 }
 
 // inv of block b's slots; block 0 writes the offsets
-__global__ __launch_bounds__(kThreads) void sort_place_kernel(SortArgs a, int slots, int blocks) {
-    constexpr int kPer = kMaxE / kThreads;
+__global__ __launch_bounds__(kPlaceThreads) void sort_place_kernel(SortArgs a, int slots, int blocks) {
+    constexpr int kPer = kMaxE / kPlaceThreads, kWaves = kPlaceThreads / 64;
     __shared__ int run[kWaves * kMaxE];     // a wave's next position in each expert
     __shared__ int before[kMaxE], total[kMaxE];
     __shared__ int s_scan[kWaves];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < kWaves * a.E; i += kThreads) run[i] = 0;
-    for (int e = threadIdx.x; e < kMaxE; e += kThreads) before[e] = total[e] = 0;
+    for (int i = threadIdx.x; i < kWaves * a.E; i += kPlaceThreads) run[i] = 0;
+    for (int e = threadIdx.x; e < kMaxE; e += kPlaceThreads) before[e] = total[e] = 0;
     __syncthreads();
-    // a wave's slots: a contiguous quarter of the block's, a multiple of 64
+    // a wave's slots: a contiguous part of the block's, a multiple of 64
     const int64_t base = int64_t(blockIdx.x) * slots + wv * (slots / kWaves);
     const int first = int(min(int64_t(a.R), base)), last = int(min(int64_t(a.R), base + slots / kWaves));
     int* const mine = run + wv * a.E;
@@ -207,11 +226,11 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortArgs a, int sl
     }
     // the blocks' counts: threads of `step` experts side by side, the rest over the blocks
     int step = 64;
-    while (step < a.E && step < kThreads) step <<= 1;
+    while (step < a.E && step < kPlaceThreads) step <<= 1;
     for (int e = threadIdx.x % step; e < a.E; e += step) {
         int b = 0, n = 0;
 #pragma unroll 8
-        for (int q = threadIdx.x / step; q < blocks; q += kThreads / step) {
+        for (int q = threadIdx.x / step; q < blocks; q += kPlaceThreads / step) {
             const int c = a.counts[int64_t(q) * a.E + e];
             n += c;
             b += q < int(blockIdx.x) ? c : 0;
@@ -239,9 +258,9 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortArgs a, int sl
         }
         at += n[i];
     }
-    if (blockIdx.x == 0 && a.E == kMaxE && threadIdx.x == kThreads - 1) a.offsets[kMaxE] = at;
+    if (blockIdx.x == 0 && a.E == kMaxE && threadIdx.x == kPlaceThreads - 1) a.offsets[kMaxE] = at;
     __syncthreads();
-    place_slots(a, first, last, mine, nullptr);
+    place_slots(a, first, last, first + lane < last ? a.ids[first + lane] : -1, mine, nullptr);
 }
 
 // ---------------------------------------------------------------------------
@@ -372,6 +391,7 @@ __global__ __launch_bounds__(kThreads) void sort_batch_kernel(SortArgs a, int pe
     for (int i = threadIdx.x; i < 2 * kMaxE; i += kThreads) count[i] = 0;
     __syncthreads();
     const int own = first * a.topk, copy = lane & ((1 << rep) - 1);
+    const int own_id = own + lane < last * a.topk ? a.ids[own + lane] : -1;
     each_id<kThreads, 8>(a.ids, a.R, threadIdx.x, [&](int i, int id) {
         if (uint32_t(id) < uint32_t(a.E)) atomicAdd(&count[((i >= own ? a.E : 0) + id << rep) + copy], 1);
     });
@@ -398,7 +418,7 @@ __global__ __launch_bounds__(kThreads) void sort_batch_kernel(SortArgs a, int pe
     }
     if (blockIdx.x == 0 && a.E == kMaxE && threadIdx.x == kThreads - 1) a.offsets[kMaxE] = at;
     __syncthreads();
-    if (wv == 0) place_slots(a, own, last * a.topk, count, pos);
+    if (wv == 0) place_slots(a, own, last * a.topk, own_id, count, pos);
     __syncthreads();
     const bool whole = u1 - u0 <= 64 * CH;                 // the part in the wave's registers
     for (int t = first + wv; t < last; t += kWaves) {
@@ -475,7 +495,7 @@ SortPlan plan_sort(int64_t R) {
     if (R <= kBatchMostSlots) return {0, 0};
     // 1024 slots a block, more where there would be over kMostBlocks of them (a
     // block reads the counts of all)
-    const int64_t slots = std::max<int64_t>(1024, (R + kMostBlocks - 1) / kMostBlocks + 255) / 256 * 256;
+    const int64_t slots = (R / kMostBlocks + kPlaceThreads) / kPlaceThreads * kPlaceThreads;
     return {int(slots), int((R + slots - 1) / slots)};
 }
 
@@ -483,7 +503,7 @@ hipError_t launch_sort_rows(const SortArgs& a, SortMode mode, hipStream_t s) {
     const SortPlan p = plan_sort(a.R);
     if (p.blocks == 0) return launch_move(a, mode, false, s);
     hipError_t e = start(sort_count_kernel, dim3(p.blocks), kThreads, s, a, p.slots);
-    if (e == hipSuccess) e = start(sort_place_kernel, dim3(p.blocks), kThreads, s, a, p.slots, p.blocks);
+    if (e == hipSuccess) e = start(sort_place_kernel, dim3(p.blocks), kPlaceThreads, s, a, p.slots, p.blocks);
     return e == hipSuccess ? launch_move(a, mode, true, s) : e;
 }
 
