@@ -22,11 +22,12 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kPlaceThreads = 1024;
-constexpr int kWaves = kThreads / 64;
 constexpr int kBatchMostSlots = 32768;
 constexpr int kMostBlocks = 256;
-// tokens of a workgroup of the batch form: a whole number to each wave, about 512
-// workgroups
+// The batch form: kTeams tokens at a time, kTeam waves to each (one wave
+// to a token 14.5 us for 1031 x 4096 to int8, two 12.7, four 12.8; 4000 tokens 36.8 / 32.7 / 31.9)
+constexpr int kTeam = 2, kTeams = 4, kBatchThreads = 64 * kTeam * kTeams;
+// tokens of its workgroup: a whole number to each team, about 512 workgroups
 constexpr int batch_tokens(int T) { return (T + 2047) / 2048 * 4; }
 // and its slots, at most kBatchMostSlots / 512 of T / 512 tokens and those of 4 more
 constexpr int kBatchSlots = kBatchMostSlots / 512 + 4 * MOE_MAX_TOPK;
@@ -366,33 +367,34 @@ __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, in
     if (kMode == kSortCopy && part == 0) copy_scales(a, token, pos, threadIdx.x, NT);
 }
 
-// Tokens first .. first + per - 1 by a workgroup, a wave to a token's row or, of
-// long rows that are not int8's, a part of `span` pieces of it.
-// The workgroup counts all ids by expert, those before its own slots apart, in
+// Tokens first .. first + per - 1 by a workgroup, kTeam waves to a token's row or,
+// of long rows that are not int8's, a part of `span` pieces of it.  The workgroup counts all ids by expert, those before its own slots apart, in
 // `1 << rep` copies (lanes of one expert add to different ones), and ranks its
 // own slots; its first rows are on their way meanwhile.
 template <SortMode kMode, int CH>
-__global__ __launch_bounds__(kThreads) void sort_batch_kernel(SortArgs a, int per, int rep, int span) {
-    constexpr int kPer = kMaxE / kThreads;
+__global__ __launch_bounds__(kBatchThreads) void sort_batch_kernel(SortArgs a, int per, int rep, int span) {
+    constexpr int NT = kBatchThreads, kPer = kMaxE / NT, kLanes = 64 * kTeam;
     __shared__ int count[2 * kMaxE];        // [before, from][E][1 << rep], then a slot's next position in each expert
     __shared__ int pos[kBatchSlots];
-    __shared__ int s_scan[kWaves];
+    __shared__ int s_scan[NT / 64];
+    __shared__ uint32_t s_max[2][NT / 64];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int team = wv / kTeam, at_row = threadIdx.x % kLanes;
     const int first = blockIdx.x * per, last = min(a.T, first + per);
     const int64_t row_bytes = int64_t(a.units) * (16 * Piece<kMode>::kLoads);
     const int u0 = int(blockIdx.y) * span, u1 = min(a.units, u0 + span);
     Piece<kMode> p[CH];
     auto load = [&](int t, int u) {                        // behind the part: its last piece again
 #pragma unroll
-        for (int c = 0; c < CH; ++c) p[c].load(a.x + t * row_bytes, min(u + lane + 64 * c, u1 - 1));
+        for (int c = 0; c < CH; ++c) p[c].load(a.x + t * row_bytes, min(u + at_row + kLanes * c, u1 - 1));
     };
-    load(min(first + wv, a.T - 1), u0);
+    load(min(first + team, a.T - 1), u0);
 
-    for (int i = threadIdx.x; i < 2 * kMaxE; i += kThreads) count[i] = 0;
+    for (int i = threadIdx.x; i < 2 * kMaxE; i += NT) count[i] = 0;
     __syncthreads();
     const int own = first * a.topk, copy = lane & ((1 << rep) - 1);
     const int own_id = own + lane < last * a.topk ? a.ids[own + lane] : -1;
-    each_id<kThreads, 8>(a.ids, a.R, threadIdx.x, [&](int i, int id) {
+    each_id<NT, 8>(a.ids, a.R, threadIdx.x, [&](int i, int id) {
         if (uint32_t(id) < uint32_t(a.E)) atomicAdd(&count[((i >= own ? a.E : 0) + id << rep) + copy], 1);
     });
     __syncthreads();
@@ -416,16 +418,17 @@ __global__ __launch_bounds__(kThreads) void sort_batch_kernel(SortArgs a, int pe
         if (e < a.E) count[e] = at + before[i];
         at += n[i];
     }
-    if (blockIdx.x == 0 && a.E == kMaxE && threadIdx.x == kThreads - 1) a.offsets[kMaxE] = at;
+    if (blockIdx.x == 0 && a.E == kMaxE && threadIdx.x == NT - 1) a.offsets[kMaxE] = at;
     __syncthreads();
     if (wv == 0) place_slots(a, own, last * a.topk, own_id, count, pos);
     __syncthreads();
-    const bool whole = u1 - u0 <= 64 * CH;                 // the part in the wave's registers
-    for (int t = first + wv; t < last; t += kWaves) {
-        bool loaded = t < first + kWaves;
+    const bool whole = u1 - u0 <= kLanes * CH;             // the part in the team's registers
+    for (int k = 0; k < per / kTeams; ++k) {               // every wave as often: there is a barrier in it
+        const int t = first + team + k * kTeams;
+        bool loaded = k == 0;
         uint32_t bits = 0;
         if constexpr (kMode == kSortInt8) {
-            for (int u = u0; u < u1; u += 64 * CH) {
+            for (int u = u0; u < u1 && t < last; u += kLanes * CH) {
                 if (!loaded) load(t, u);
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
@@ -433,14 +436,19 @@ __global__ __launch_bounds__(kThreads) void sort_batch_kernel(SortArgs a, int pe
                 loaded = whole;
             }
             bits = wave_max_u16(bits);
+            if (lane == 0) s_max[k & 1][wv] = bits;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kTeam; ++i) bits = max(bits, s_max[k & 1][team * kTeam + i]);
         }
+        if (t >= last) continue;
         const int* mine = pos + (t - first) * a.topk;
-        for (int u = u0; u < u1; u += 64 * CH) {
+        for (int u = u0; u < u1; u += kLanes * CH) {
             if (!loaded) load(t, u);
-            store_pieces<kMode, CH>(a, p, mine, u + lane, u1, 64, bits);
+            store_pieces<kMode, CH>(a, p, mine, u + at_row, u1, kLanes, bits);
             loaded = false;
         }
-        if (kMode == kSortCopy && u0 == 0) copy_scales(a, t, mine, lane, 64);
+        if (kMode == kSortCopy && u0 == 0) copy_scales(a, t, mine, at_row, kLanes);
     }
 }
 
@@ -451,21 +459,21 @@ hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
     const int span = kMode == kSortInt8 ? a.units : kSpan;
     int rep = 0;
     while (rep < 3 && (2 * a.E << (rep + 1)) <= 2 * kMaxE) ++rep;
-    void (*kern)(SortArgs, int, int, int) = a.units <= 64    ? sort_batch_kernel<kMode, 1>
-                                       : a.units <= 128 ? sort_batch_kernel<kMode, 2>
-                                       : a.units <= 256 ? sort_batch_kernel<kMode, 4>
-                                       : a.units <= 512 || kMode != kSortCopy ? sort_batch_kernel<kMode, 8>
-                                                                              : sort_batch_kernel<kMode, 16>;
+    const int per_lane = (std::min(a.units, span) + 64 * kTeam - 1) / (64 * kTeam);
+    void (*kern)(SortArgs, int, int, int) = per_lane <= 1   ? sort_batch_kernel<kMode, 1>
+                                            : per_lane <= 2 ? sort_batch_kernel<kMode, 2>
+                                            : per_lane <= 4 ? sort_batch_kernel<kMode, 4> : sort_batch_kernel<kMode, 8>;
     const dim3 grid((a.T + per - 1) / per, (a.units + span - 1) / span);
-    return start(kern, grid, kThreads, s, a, per, rep, span);
+    return start(kern, grid, kBatchThreads, s, a, per, rep, span);
 }
 
 // Whether few ids are read so few times that every workgroup may compare them all
 // (sort_move_kernel<.., true>): ids read in all, us in that form / in the batch
-// form: 512 tokens of 4096 to 8 experts, to int8 (2.1 M) 8.7 / 9.9, 300 of 7168
-// in four parts (2.9 M) 11.5 / 12.9, 512 of 7168 (8.4 M) 17.5 / 15.7, 1031 of
-// 4096 to int8 (8.5 M) 19.3 / 14.5.  Few tokens do not fill the batch form's waves.
-bool few_ids(const SortArgs& a, int parts) { return a.T <= 256 || int64_t(a.T) * parts * a.R <= 4 << 20; }
+// form: 512 tokens of 4096 to 8 experts, to int8 (2.0 M) 8.8 / 9.2, 256 of 7168 in
+// four parts (2.0 M) 9.5 / 11.5, 300 (2.8 M) 11.3 / 12.0; 600 to int8 (2.8 M) 11.6 /
+// 9.6, 700 (3.7 M) 12.4 / 10.1, 1031 (8.5 M) 19.3 / 12.7.  Few tokens do not fill the
+// batch form's waves.
+bool few_ids(const SortArgs& a, int parts) { return a.T <= 256 || int64_t(a.T) * parts * a.R <= 5 << 19; }
 
 template <SortMode kMode, int NT, int CH>
 hipError_t launch_move(const SortArgs& a, bool counted, hipStream_t s) {

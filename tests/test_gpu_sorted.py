@@ -134,7 +134,8 @@ def test_sort_rows_long_rows_of_many_tokens(cols, kind, quant):
     check_sort(1100, 4, 9, cols, kind, quant, routing(rng, 1100, 4, 9, away=0.3), cols)
 
 
-@pytest.mark.parametrize("T,k", [(1448, 1), (1449, 1), (511, 8), (513, 8), (724, 4), (725, 4), (2051, 8), (4095, 7)])
+@pytest.mark.parametrize("T,k", [(1619, 1), (1620, 1), (572, 8), (573, 8), (809, 4), (810, 4), (257, 64),
+                                 (2051, 8), (4095, 7)])
 def test_sort_rows_between_the_forms(T, k):
     """Batches around the size from which tokens share a workgroup, and of several tokens a wave."""
     rng = np.random.default_rng(T)
