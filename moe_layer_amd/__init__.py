@@ -7,8 +7,9 @@ router-weighted combine) runs in hand-written HIP kernels behind the C ABI of
 around it: the quantising residual-add + RMSNorm, the quantising SiLU-gated
 multiply, the dense block-scaled fp8 product, the dense int8 product and the
 ragged products grouped by expert, tokens' rows sorted by expert and combined
-again (with the gradients), and rows quantised to int8.  ``moe_layer_amd.ops`` is the thin Python binding with the same
-entry-point names; importing this package does not load the library.
+again (with the gradients), and rows quantised to int8.  ``moe_layer_amd.ops``
+is the thin Python binding with the same entry-point names; importing this
+package does not load the library.
 """
 
 __all__ = ["ops", "workloads"]

@@ -4,6 +4,9 @@
 //   grad_weights[t, j] = sum_h grad_out[t, h] rows[inv[t, j], h]   (fp32)
 // A slot whose inv lies outside [0, num_rows) has no row: it adds nothing, and
 // its weight's gradient is 0.
+//
+// Every row is read once, and what is written is written once: both are bound by
+// bytes.  @@
 #include "sorted.h"
 
 namespace moe {
@@ -162,8 +165,10 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void combine_rows_bwd_kernel
 template <int W, bool kDots, bool kWeights>
 hipError_t launch_bwd(const CombineArgs& a, hipStream_t s) {
     constexpr int NT = W <= 4 ? 256 : 64 * W, kTokens = NT / 64 / W;
-    return start(combine_rows_bwd_kernel<W, kDots, kWeights>, grid_of((int64_t(a.T) + kTokens - 1) / kTokens), NT, s, a);
+    const int64_t n = (int64_t(a.T) + kTokens - 1) / kTokens;
+    return start(combine_rows_bwd_kernel<W, kDots, kWeights>, grid_of(n), NT, s, a);
 }
+
 // Columns up to which a wave takes a token (us, one wave / four: 2048 tokens of 256
 // and 8 slots 5.7 / 9.1, of 512 7.1 / 10.0, of 1024 14.3 / 14.3, of 4096 48 / 47), and
 // tokens up to which sixteen waves do (four / sixteen: 64 x 7168 7.7 / 7.1, 200 x 7168

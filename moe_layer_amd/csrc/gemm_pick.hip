@@ -123,7 +123,8 @@ RowsPlan plan_rows_gemm(const RowsGemmArgs& g, RowsKind kind) {
 
 hipError_t launch_rows_gemm(const RowsGemmArgs& g, RowsKind kind, hipStream_t s) {
     const RowsPlan p = plan_rows_gemm(g, kind);
-    return p.split ? launch_rows_split(g, kind, p.shape, p.one_pass, s) : launch_rows_tile(g, kind, p.shape, p.one_pass, s);
+    return p.split ? launch_rows_split(g, kind, p.shape, p.one_pass, s)
+                   : launch_rows_tile(g, kind, p.shape, p.one_pass, s);
 }
 
 }  // namespace moe

@@ -5,7 +5,8 @@
 //
 // A row is held in the registers of W waves, CH chunks of 8 columns a lane, so
 // it is read once; the maximum of the row's bf16 bits is joined through lane
-// permutations and, for W > 1, LDS.
+// permutations and, for W > 1, LDS.  Many rows are bound by their bytes (5.1 TB/s,
+// the rate of a large copy), few by the launch (3.6-4 us).
 #include "moe.h"
 
 #include "dev_silu.h"
@@ -57,28 +58,36 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void quant_int8_kernel(Int8A
     if (tid == 0) a.scales[row] = scale;
 }
 
-// Rows from which a wave takes a whole row
+// Rows from which a wave takes a whole row, up to kWaveVecs chunks of 8 columns; below
+// it four waves do, which need less time for a row.  us, one wave / four, outputs that
+// stay in the caches: gated, 128 rows of 4096 5.0 / 3.7, 512 of 2560 4.4 / 3.9, 1536 of
+// 2048 5.2 / 4.8, 2048 of 2560 6.9 / 8.4, 16384 of 1536 22.9 / 28.4, of 2560 39.3 / 47.1,
+// of 4096, gate and up half in 64 registers each, 64.6 / 60.9; not gated, 16384 of 1536
+// 12.0 / 12.6, of 4096 29.4 / 28.6, 4096 of 4096 8.0 / 9.1.
 constexpr int kManyRows = 2048;
+template <bool kGated>
+constexpr int kWaveVecs = kGated ? 384 : 512;
 
 template <bool kGated, bool kClamp>
 hipError_t launch(const Int8Args& a, hipStream_t s) {
     auto go = [&](auto w, auto ch) {
         constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
         constexpr int NT = W <= 4 ? 256 : 64 * W, kRows = NT / 64 / W;
-        return start(quant_int8_kernel<W, CH, kGated, kClamp>, grid_of((int64_t(a.rows) + kRows - 1) / kRows), NT, s, a);
+        const int64_t n = (int64_t(a.rows) + kRows - 1) / kRows;
+        return start(quant_int8_kernel<W, CH, kGated, kClamp>, grid_of(n), NT, s, a);
     };
     using std::integral_constant;
     using One = integral_constant<int, 1>;
     using Four = integral_constant<int, 4>;
     using Sixteen = integral_constant<int, 16>;
     const int nvec = a.cols >> 3;
-    if (a.rows >= kManyRows) {
+    if (a.rows >= kManyRows && nvec <= kWaveVecs<kGated>) {
         if (nvec <= 64) return go(One(), One());
         if (nvec <= 128) return go(One(), integral_constant<int, 2>());
         if (nvec <= 192) return go(One(), integral_constant<int, 3>());
         if (nvec <= 256) return go(One(), Four());
         if (nvec <= 384) return go(One(), integral_constant<int, 6>());
-        if (nvec <= 512) return go(One(), integral_constant<int, 8>());
+        if constexpr (!kGated) return go(One(), integral_constant<int, 8>());
     }
     if (nvec <= 64) return go(One(), One());
     if (nvec <= 256) return go(Four(), One());

@@ -533,8 +533,9 @@ def moe_grouped_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, a_
     """Products of rows sorted by expert, group e being rows offsets[e] ..
     offsets[e+1] (int32 [E+1] on the device): bf16 a [rows, K] and w [E, N, K],
     e4m3 ones with fp32 a_scale [rows, K/128] and w_scale [E, ceil(N/128),
-    K/128], or int8 ones with fp32 a_scale [rows] and w_scale [E, N].  Returns bf16 out [rows, N]; rows outside every group keep what
-    out held (uninitialised when it is allocated here)."""
+    K/128], or int8 ones with fp32 a_scale [rows] and w_scale [E, N].  Returns
+    bf16 out [rows, N]; rows outside every group keep what out held
+    (uninitialised when it is allocated here)."""
     return _call("grouped_gemm", a, w, offsets, a_scale, w_scale, out)
 
 
