@@ -92,11 +92,15 @@ double time_us(const Tile& t, const RowsGemmArgs& g, RowsKind kind) {
 // (15 MB) 6.3 / 7.2, 8 x 20000 x 7168 (143 MB) 31.0 / 27.6; 131 fp8 rows in 32
 // groups of 4096 x 2048 (268 MB) 49.4 / 44.1; 8192 in 256 groups of 512 x 4096,
 // half-full 64-row blocks 142 / 136; 32768 bf16 rows in 128 groups of 4096 x 1536,
-// as many as fill a 256-row block each 518 / 545.
+// as many as fill a 256-row block each 518 / 545.  Not where K (int8) is no whole
+// number of lines: two steps have a part of each line, and the second would fetch it
+// again (6059 rows in 128 groups of 2568 x 3056 254 / 345; 1 x 20000 x 7184 25.8 /
+// 37.5; 300 in 128 of 2048 x 2064 78 / 88).
 bool one_pass(const RowsGemmArgs& g, int bm, RowsKind kind) {
     const int64_t groups = g.offsets ? std::min(g.E, g.rows) : 1;
     const int64_t rows = g.offsets ? 2 * int64_t(g.rows) : g.rows;
-    return rows <= bm * groups && groups * g.N * g.K * (kind == kRowsBf16 ? 2 : 1) >= int64_t(128) << 20;
+    const int64_t row_bytes = g.K * (kind == kRowsBf16 ? 2 : 1);
+    return rows <= bm * groups && groups * g.N * row_bytes >= int64_t(128) << 20 && row_bytes % 128 == 0;
 }
 
 template <int N>

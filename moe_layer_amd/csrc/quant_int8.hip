@@ -3,9 +3,9 @@
 //   m = max(|v|max, 1e-10), scale = fl32(m / 127), code = RNE(v fl32(127 / m)),
 //   gated: v = bf16(bf16(silu(g)) * u) after the optional clamp (dev_silu.h).
 //
-// A row is held in the registers of W waves, CH chunks of 8 columns a lane, so
-// it is read once; the maximum of the row's bf16 bits is joined through lane
-// permutations and, for W > 1, LDS.  Many rows are bound by their bytes (5.1 TB/s,
+// A row is held in the registers of L lanes, CH chunks of 8 columns each, so it is
+// read once; the maximum of the row's bf16 bits is joined through lane permutations
+// and, where several waves have a row, LDS.  Many rows are bound by their bytes (5.1 TB/s,
 // the rate of a large copy), few by the launch (3.6-4 us).
 #include "moe.h"
 
@@ -16,20 +16,24 @@ namespace moe {
 
 namespace {
 
-template <int W, int CH, bool kGated, bool kClamp>
-__global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void quant_int8_kernel(Int8Args a) {
-    constexpr int NT = W <= 4 ? 256 : 64 * W, kRows = NT / 64 / W;
+// threads of a workgroup whose rows are L lanes' each
+template <int L>
+constexpr int kThreads = L <= 256 ? 256 : L;
+
+template <int L, int CH, bool kGated, bool kClamp>
+__global__ __launch_bounds__(kThreads<L>) void quant_int8_kernel(Int8Args a) {
+    constexpr int NT = kThreads<L>;
     __shared__ uint32_t s_max[NT / 64];
     const int64_t wg = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
-    const int64_t mine = wg * kRows + threadIdx.x / (64 * W);
-    if (W == 1 && mine >= a.rows) return;
+    const int64_t mine = wg * (NT / L) + threadIdx.x / L;
+    if (L == 64 && mine >= a.rows) return;
     const int64_t row = min(mine, int64_t(a.rows) - 1);
-    const int tid = threadIdx.x % (64 * W), nvec = a.cols >> 3;
+    const int tid = threadIdx.x % L, nvec = a.cols >> 3;
     const uint16_t* x = a.x + row * a.cols * (kGated ? 2 : 1);
     i32x4 v[CH], u[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int i = min(tid + c * 64 * W, nvec - 1);     // behind the row: its last chunk again
+        const int i = min(tid + c * L, nvec - 1);     // behind the row: its last chunk again
         v[c] = *reinterpret_cast<const i32x4*>(x + i * 8);
         if constexpr (kGated) u[c] = *reinterpret_cast<const i32x4*>(x + a.cols + i * 8);
     }
@@ -39,20 +43,20 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void quant_int8_kernel(Int8A
         if constexpr (kGated) v[c] = silu_mul8<kClamp>(v[c], u[c], a.limit);
         most = pk_max_u16(most, abs_max8(v[c]));
     }
-    uint32_t bits = wave_max_u16(most);
-    if constexpr (W > 1) {
+    uint32_t bits = lanes_max_u16<(L < 64 ? L : 64)>(most);
+    if constexpr (L > 64) {
         if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = bits;
         __syncthreads();
-        const int first = threadIdx.x / (64 * W) * W;
+        const int first = threadIdx.x / L * (L / 64);
 #pragma unroll
-        for (int i = 0; i < W; ++i) bits = max(bits, s_max[first + i]);
+        for (int i = 0; i < L / 64; ++i) bits = max(bits, s_max[first + i]);
     }
     float inverse;
     const float scale = int8_scale(bits, inverse);
     if (mine >= a.rows) return;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int i = tid + c * 64 * W;
+        const int i = tid + c * L;
         if (i < nvec) *reinterpret_cast<uint2*>(a.codes + row * a.cols + i * 8) = int8_codes(v[c], inverse);
     }
     if (tid == 0) a.scales[row] = scale;
@@ -70,32 +74,36 @@ constexpr int kWaveVecs = kGated ? 384 : 512;
 
 template <bool kGated, bool kClamp>
 hipError_t launch(const Int8Args& a, hipStream_t s) {
-    auto go = [&](auto w, auto ch) {
-        constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
-        constexpr int NT = W <= 4 ? 256 : 64 * W, kRows = NT / 64 / W;
+    auto go = [&](auto lanes, auto ch) {
+        constexpr int L = decltype(lanes)::value, CH = decltype(ch)::value, kRows = kThreads<L> / L;
         const int64_t n = (int64_t(a.rows) + kRows - 1) / kRows;
-        return start(quant_int8_kernel<W, CH, kGated, kClamp>, grid_of(n), NT, s, a);
+        return start(quant_int8_kernel<L, CH, kGated, kClamp>, grid_of(n), kThreads<L>, s, a);
     };
     using std::integral_constant;
-    using One = integral_constant<int, 1>;
-    using Four = integral_constant<int, 4>;
-    using Sixteen = integral_constant<int, 16>;
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    const integral_constant<int, 4> four;
+    const integral_constant<int, 64> wave;
+    const integral_constant<int, 256> waves4;
+    const integral_constant<int, 1024> waves16;
     const int nvec = a.cols >> 3;
+    if (nvec <= 8) return go(integral_constant<int, 8>(), one);
+    if (nvec <= 16) return go(integral_constant<int, 16>(), one);
+    if (nvec <= 32) return go(integral_constant<int, 32>(), one);
+    if (nvec <= 64) return go(wave, one);
     if (a.rows >= kManyRows && nvec <= kWaveVecs<kGated>) {
-        if (nvec <= 64) return go(One(), One());
-        if (nvec <= 128) return go(One(), integral_constant<int, 2>());
-        if (nvec <= 192) return go(One(), integral_constant<int, 3>());
-        if (nvec <= 256) return go(One(), Four());
-        if (nvec <= 384) return go(One(), integral_constant<int, 6>());
-        if constexpr (!kGated) return go(One(), integral_constant<int, 8>());
+        if (nvec <= 128) return go(wave, two);
+        if (nvec <= 192) return go(wave, integral_constant<int, 3>());
+        if (nvec <= 256) return go(wave, four);
+        if (nvec <= 384) return go(wave, integral_constant<int, 6>());
+        if constexpr (!kGated) return go(wave, integral_constant<int, 8>());
     }
-    if (nvec <= 64) return go(One(), One());
-    if (nvec <= 256) return go(Four(), One());
-    if (nvec <= 512) return go(Four(), integral_constant<int, 2>());
-    if (nvec <= 1024) return go(Four(), Four());
-    if (nvec <= 2048) return go(Sixteen(), integral_constant<int, 2>());
+    if (nvec <= 256) return go(waves4, one);
+    if (nvec <= 512) return go(waves4, two);
+    if (nvec <= 1024) return go(waves4, four);
+    if (nvec <= 2048) return go(waves16, two);
     static_assert(MOE_MAX_INT8_K <= 1024 * 4 * 8, "a row in one workgroup's registers");
-    return go(Sixteen(), Four());
+    return go(waves16, four);
 }
 
 }  // namespace

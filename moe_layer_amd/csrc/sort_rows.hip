@@ -28,10 +28,8 @@ constexpr int kThreads = 256, kPlaceThreads = 1024;
 // 8000 74.7 / 69.7, 133 / 125, 35.1 / 33.4.
 constexpr int kBatchMostSlots = 32768;
 constexpr int kMostBlocks = 256;
-// The batch form: kTeams tokens at a time, kTeam waves to each (one wave to a token
-// 14.5 us for 1031 x 4096 to int8, two 12.7, four 12.8; 4000 tokens 36.8 / 32.7 / 31.9)
-constexpr int kTeam = 2, kTeams = 4, kBatchThreads = 64 * kTeam * kTeams;
-// tokens of its workgroup: a whole number to each team, about 512 workgroups
+constexpr int kBatchThreads = 512;
+// tokens of a workgroup of the batch form: about 512 workgroups
 constexpr int batch_tokens(int T) { return (T + 2047) / 2048 * 4; }
 // and its slots, at most kBatchMostSlots / 512 of T / 512 tokens and those of 4 more
 constexpr int kBatchSlots = kBatchMostSlots / 512 + 4 * MOE_MAX_TOPK;
@@ -285,8 +283,9 @@ struct Piece {
 
 // the row's pieces u0, u0 + stride, .. below u1 (CH of them in p) to the
 // positions of the token's slots.  kSortInt8: bits is the row's largest magnitude;
-// kSortFp8: a lane's piece and its neighbours' make whole groups.
-template <SortMode kMode, int CH>
+// kSortFp8: a lane's piece and its neighbours' make whole groups.  kWaves: a wave's
+// lanes have one token.
+template <SortMode kMode, int CH, bool kWaves = true>
 __device__ __forceinline__ void store_pieces(const SortArgs& a, const Piece<kMode> (&p)[CH], const int* pos, int u0,
                                              int u1, int stride, uint32_t bits) {
     i32x4 out[CH];
@@ -304,7 +303,7 @@ __device__ __forceinline__ void store_pieces(const SortArgs& a, const Piece<kMod
         }
     }
     for (int j = 0; j < a.topk; ++j) {
-        const int at = __builtin_amdgcn_readfirstlane(pos[j]);
+        const int at = kWaves ? __builtin_amdgcn_readfirstlane(pos[j]) : pos[j];
         if (at < 0) continue;
         uint8_t* to = a.rows + int64_t(at) * a.units * 16;
 #pragma unroll
@@ -319,10 +318,14 @@ __device__ __forceinline__ void store_pieces(const SortArgs& a, const Piece<kMod
     }
 }
 
-// the scales of a token's codes, by `lanes` lanes
-__device__ __forceinline__ void copy_scales(const SortArgs& a, int64_t token, const int* pos, int lane, int lanes) {
+// the scales of a token's codes by `lanes` lanes, whose first ones were read ahead
+__device__ __forceinline__ float first_scale(const SortArgs& a, int64_t token, int lane) {
+    return lane < a.scales ? a.x_scale[token * a.scales + lane] : 0.0f;
+}
+__device__ __forceinline__ void copy_scales(const SortArgs& a, int64_t token, const int* pos, int lane, int lanes,
+                                            float first) {
     for (int i = lane; i < a.scales; i += lanes) {
-        const float s = a.x_scale[token * a.scales + i];
+        const float s = i == lane ? first : a.x_scale[token * a.scales + i];
         for (int j = 0; j < a.topk; ++j)
             if (pos[j] >= 0) a.row_scales[int64_t(pos[j]) * a.scales + i] = s;
     }
@@ -346,6 +349,7 @@ __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, in
 #pragma unroll
     for (int c = 0; c < CH; ++c)                           // behind the part: its last piece again
         p[c].load(a.x + token * a.units * (16 * Piece<kMode>::kLoads), min(u0 + c * NT, u1 - 1));
+    const float scale = kMode == kSortCopy && part == 0 ? first_scale(a, token, threadIdx.x) : 0.0f;
     if constexpr (kOne) {
         if (threadIdx.x < unsigned(a.topk)) pos[threadIdx.x] = 0;
         __syncthreads();
@@ -357,7 +361,7 @@ __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, in
     if constexpr (kMode == kSortInt8) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) bits = pk_max_u16(bits, pk_max_u16(abs_max8(p[c].v[0]), abs_max8(p[c].v[1])));
-        bits = wave_max_u16(bits);
+        bits = lanes_max_u16<64>(bits);
         if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = bits;
     }
     __syncthreads();
@@ -368,30 +372,52 @@ __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, in
         for (int i = 0; i < NT / 64; ++i) bits = max(bits, s_max[i]);
     }
     store_pieces<kMode, CH>(a, p, pos, u0, u1, NT, bits);
-    if (kMode == kSortCopy && part == 0) copy_scales(a, token, pos, threadIdx.x, NT);
+    if (kMode == kSortCopy && part == 0) copy_scales(a, token, pos, threadIdx.x, NT, scale);
 }
 
-// Tokens first .. first + per - 1 by a workgroup, kTeam waves to a token's row or,
-// of long rows that are not int8's, a part of `span` pieces of it.  The workgroup
-// counts all ids by expert, those before its own slots apart, in `1 << rep` copies
-// (lanes of one expert add to different ones), and ranks its own slots; its first
-// rows are on their way meanwhile.
-template <SortMode kMode, int CH>
+// The counted form's rows of L pieces or fewer, L lanes to a token
+template <SortMode kMode, int L>
+__global__ __launch_bounds__(kThreads) void sort_narrow_kernel(SortArgs a) {
+    const int64_t wg = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t mine = wg * (kThreads / L) + threadIdx.x / L, token = min(mine, int64_t(a.T) - 1);
+    const int u = threadIdx.x % L;
+    Piece<kMode> p[1];
+    p[0].load(a.x + token * a.units * (16 * Piece<kMode>::kLoads), min(u, a.units - 1));
+    const float scale = kMode == kSortCopy ? first_scale(a, token, u) : 0.0f;
+    uint32_t bits = 0;
+    if constexpr (kMode == kSortInt8)
+        bits = lanes_max_u16<L>(pk_max_u16(abs_max8(p[0].v[0]), abs_max8(p[0].v[1])));
+    if (mine >= a.T) return;
+    const int* const pos = a.inv + token * a.topk;
+    store_pieces<kMode, 1, false>(a, p, pos, u, a.units, L, bits);
+    if (kMode == kSortCopy) copy_scales(a, token, pos, u, L, scale);
+}
+
+// Tokens first .. first + per - 1 by a workgroup, L lanes to a token's row (up to 64
+// for one of as many pieces or fewer) or, of long rows that are not int8's, a part of
+// `span` pieces of it.  The workgroup counts all ids by expert, those before its own
+// slots apart, in `1 << rep` copies (lanes of one expert add to different ones), and
+// ranks its own slots; its first rows are on their way meanwhile.  Two waves to a long
+// row: 1031 x 4096 to int8 12.7 us, one 14.5, four 12.8; 4000 tokens 32.7 / 36.8 / 31.9.
+template <SortMode kMode, int CH, int L>
 __global__ __launch_bounds__(kBatchThreads) void sort_batch_kernel(SortArgs a, int per, int rep, int span) {
-    constexpr int NT = kBatchThreads, kPer = kMaxE / NT, kLanes = 64 * kTeam;
+    constexpr int NT = kBatchThreads, kPer = kMaxE / NT, kTeams = NT / L, kWaves = L / 64;
+    static_assert(L <= 64 ? CH == 1 : L % 64 == 0, "lanes");
     __shared__ int count[2 * kMaxE];        // [before, from][E][1 << rep], then a slot's next position in each expert
     __shared__ int pos[kBatchSlots];
     __shared__ int s_scan[NT / 64];
     __shared__ uint32_t s_max[2][NT / 64];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int team = wv / kTeam, at_row = threadIdx.x % kLanes;
+    const int team = L >= 64 ? wv / kWaves : int(threadIdx.x) / L, at_row = threadIdx.x % L;
     const int first = blockIdx.x * per, last = min(a.T, first + per);
     const int64_t row_bytes = int64_t(a.units) * (16 * Piece<kMode>::kLoads);
     const int u0 = int(blockIdx.y) * span, u1 = min(a.units, u0 + span);
     Piece<kMode> p[CH];
+    float scale = 0.0f;
     auto load = [&](int t, int u) {                        // behind the part: its last piece again
 #pragma unroll
-        for (int c = 0; c < CH; ++c) p[c].load(a.x + t * row_bytes, min(u + at_row + kLanes * c, u1 - 1));
+        for (int c = 0; c < CH; ++c) p[c].load(a.x + t * row_bytes, min(u + at_row + L * c, u1 - 1));
+        if (kMode == kSortCopy && u == 0) scale = first_scale(a, t, at_row);
     };
     load(min(first + team, a.T - 1), u0);
 
@@ -427,33 +453,35 @@ __global__ __launch_bounds__(kBatchThreads) void sort_batch_kernel(SortArgs a, i
     __syncthreads();
     if (wv == 0) place_slots(a, own, last * a.topk, own_id, count, pos);
     __syncthreads();
-    const bool whole = u1 - u0 <= kLanes * CH;             // the part in the team's registers
-    for (int k = 0; k < per / kTeams; ++k) {               // every wave as often: there is a barrier in it
+    const bool whole = u1 - u0 <= L * CH;                  // the part in the team's registers
+    for (int k = 0; k * kTeams < per; ++k) {               // every wave as often: there is a barrier in it
         const int t = first + team + k * kTeams;
         bool loaded = k == 0;
         uint32_t bits = 0;
         if constexpr (kMode == kSortInt8) {
-            for (int u = u0; u < u1 && t < last; u += kLanes * CH) {
+            for (int u = u0; u < u1 && t < last; u += L * CH) {
                 if (!loaded) load(t, u);
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
                     bits = pk_max_u16(bits, pk_max_u16(abs_max8(p[c].v[0]), abs_max8(p[c].v[1])));
                 loaded = whole;
             }
-            bits = wave_max_u16(bits);
-            if (lane == 0) s_max[k & 1][wv] = bits;
-            __syncthreads();
+            bits = lanes_max_u16<(L < 64 ? L : 64)>(bits);
+            if constexpr (L > 64) {
+                if (lane == 0) s_max[k & 1][wv] = bits;
+                __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kTeam; ++i) bits = max(bits, s_max[k & 1][team * kTeam + i]);
+                for (int i = 0; i < kWaves; ++i) bits = max(bits, s_max[k & 1][team * kWaves + i]);
+            }
         }
         if (t >= last) continue;
         const int* mine = pos + (t - first) * a.topk;
-        for (int u = u0; u < u1; u += kLanes * CH) {
+        for (int u = u0; u < u1; u += L * CH) {
             if (!loaded) load(t, u);
-            store_pieces<kMode, CH>(a, p, mine, u + at_row, u1, kLanes, bits);
+            store_pieces<kMode, CH, L >= 64>(a, p, mine, u + at_row, u1, L, bits);
             loaded = false;
         }
-        if (kMode == kSortCopy && u0 == 0) copy_scales(a, t, mine, at_row, kLanes);
+        if (kMode == kSortCopy && u0 == 0) copy_scales(a, t, mine, at_row, L, scale);
     }
 }
 
@@ -464,10 +492,15 @@ hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
     const int span = kMode == kSortInt8 ? a.units : kSpan;
     int rep = 0;
     while (rep < 3 && (2 * a.E << (rep + 1)) <= 2 * kMaxE) ++rep;
-    const int per_lane = (std::min(a.units, span) + 64 * kTeam - 1) / (64 * kTeam);
-    void (*kern)(SortArgs, int, int, int) = per_lane <= 1   ? sort_batch_kernel<kMode, 1>
-                                            : per_lane <= 2 ? sort_batch_kernel<kMode, 2>
-                                            : per_lane <= 4 ? sort_batch_kernel<kMode, 4> : sort_batch_kernel<kMode, 8>;
+    const int most = std::min(a.units, span);
+    void (*kern)(SortArgs, int, int, int) = most <= 8     ? sort_batch_kernel<kMode, 1, 8>
+                                            : most <= 16  ? sort_batch_kernel<kMode, 1, 16>
+                                            : most <= 32  ? sort_batch_kernel<kMode, 1, 32>
+                                            : most <= 64  ? sort_batch_kernel<kMode, 1, 64>
+                                            : most <= 128 ? sort_batch_kernel<kMode, 1, 128>
+                                            : most <= 256 ? sort_batch_kernel<kMode, 2, 128>
+                                            : most <= 512 ? sort_batch_kernel<kMode, 4, 128>
+                                                          : sort_batch_kernel<kMode, 8, 128>;
     const dim3 grid((a.T + per - 1) / per, (a.units + span - 1) / span);
     return start(kern, grid, kBatchThreads, s, a, per, rep, span);
 }
@@ -480,12 +513,22 @@ hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
 // batch form's waves.
 bool few_ids(const SortArgs& a, int parts) { return a.T <= 256 || int64_t(a.T) * parts * a.R <= 5 << 19; }
 
+template <SortMode kMode>
+hipError_t launch_narrow(const SortArgs& a, hipStream_t s) {
+    const int lanes = a.units <= 8 ? 8 : a.units <= 16 ? 16 : a.units <= 32 ? 32 : 64;
+    void (*kern)(SortArgs) = lanes == 8    ? sort_narrow_kernel<kMode, 8>
+                             : lanes == 16 ? sort_narrow_kernel<kMode, 16>
+                             : lanes == 32 ? sort_narrow_kernel<kMode, 32> : sort_narrow_kernel<kMode, 64>;
+    return start(kern, grid_of((int64_t(a.T) * lanes + kThreads - 1) / kThreads), kThreads, s, a);
+}
+
 template <SortMode kMode, int NT, int CH>
 hipError_t launch_move(const SortArgs& a, bool counted, hipStream_t s) {
     // parts of at most NT * CH pieces, of equal length but for the rounding to whole groups
     const int parts = kMode == kSortInt8 ? 1 : (a.units + NT * CH - 1) / (NT * CH);
     const int span = kMode == kSortInt8 ? a.units : ((a.units + parts - 1) / parts + 7) / 8 * 8;
     if (!counted && !few_ids(a, parts)) return launch_batch<kMode>(a, s);
+    if (counted && a.units <= 64) return launch_narrow<kMode>(a, s);
     const int64_t n = int64_t(a.T) * parts + (counted ? 0 : 1);
     void (*kern)(SortArgs, int, int) =
         counted ? sort_move_kernel<kMode, NT, CH, false> : sort_move_kernel<kMode, NT, CH, true>;

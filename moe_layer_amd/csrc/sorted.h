@@ -69,17 +69,23 @@ __device__ __forceinline__ uint32_t abs_max8(const i32x4& w) {
     return pk_max_u16(pk_max_u16(uint32_t(w[0]) & kAbs, uint32_t(w[1]) & kAbs),
                       pk_max_u16(uint32_t(w[2]) & kAbs, uint32_t(w[3]) & kAbs));
 }
-// the largest half of a wave's words, in every lane; the bits of a bf16 without
-// their sign order as the magnitudes do
-__device__ __forceinline__ uint32_t wave_max_u16(uint32_t m) {
+// the largest half of L neighbouring lanes' words, in each of them; the bits of a
+// bf16 without their sign order as the magnitudes do
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max_u16(uint32_t m) {
+    static_assert(L == 8 || L == 16 || L == 32 || L == 64, "lanes");
     m = dpp_max_u16<0xb1>(m);                              // quad_perm [1,0,3,2]
     m = dpp_max_u16<0x4e>(m);                              // quad_perm [2,3,0,1]
     m = dpp_max_u16<0x141>(m);                             // row_half_mirror
-    m = dpp_max_u16<0x140>(m);                             // row_mirror
-    const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-    m = pk_max_u16(a[0], a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-    m = pk_max_u16(b[0], b[1]);
+    if constexpr (L > 8) m = dpp_max_u16<0x140>(m);        // row_mirror
+    if constexpr (L > 16) {
+        const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+        m = pk_max_u16(a[0], a[1]);
+    }
+    if constexpr (L > 32) {
+        const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+        m = pk_max_u16(b[0], b[1]);
+    }
     return max(m & 0xffffu, m >> 16);
 }
 // scale and inverse from the row's largest magnitude (its bf16 bits); a row with

@@ -27,7 +27,8 @@ def same_bits(a, b):
 
 ROWS = [(1, 16), (3, 48), (5, 512), (2, 528), (7, 1024), (4, 1040), (129, 1536), (9, 2048), (6, 2064), (3, 4096),
         (2, 4112), (3, 8192), (2, 8208), (2, 16384), (1, 16400), (2, 32768), (1031, 64),
-        (2047, 1008), (2050, 48), (2049, 1008), (2051, 1296), (2048, 2032), (2050, 2576), (2053, 3104), (2048, 4112)]
+        (5, 64), (7, 80), (9, 128), (17, 144), (9, 256), (5, 272), (2047, 1008), (2050, 48), (2049, 1008),
+        (2051, 1296), (2048, 2032), (2050, 2576), (2053, 3104), (2048, 4112)]
 
 
 @pytest.mark.parametrize("rows,cols", ROWS)

@@ -142,6 +142,23 @@ def test_sort_rows_between_the_forms(T, k):
     check_sort(T, k, 33, 64, "bf16", "int8", routing(rng, T, k, 33, away=0.1), T)
 
 
+# columns whose rows are up to 8, 16, 32, 64 and more pieces of 16 stored bytes
+NARROW = {("bf16", None): (8, 64, 72, 256, 504, 512, 520), ("bf16", "int8"): (16, 128, 144, 400, 512, 528, 1024, 1040),
+          ("bf16", "fp8"): (128, 256, 384, 512, 896, 1152), ("fp8", None): (128, 256, 384, 512, 1024, 1152),
+          ("int8", None): (16, 128, 144, 256, 496, 1024, 1040)}
+
+
+@pytest.mark.parametrize("kind,quant", KINDS)
+@pytest.mark.parametrize("T,k", [(2501, 3), (6260, 4), (8193, 4), (11001, 3)])
+def test_sort_rows_narrow(T, k, kind, quant):
+    """Rows that a part of a wave takes, in the two forms for many ids; the last
+    tokens leave lanes of a wave without one."""
+    rng = np.random.default_rng(T + k)
+    ids = routing(rng, T, k, 20, away=0.2)
+    for cols in NARROW[kind, quant]:
+        check_sort(T, k, 20, cols, kind, quant, ids, cols)
+
+
 def test_sort_rows_ids_anywhere():
     """Ids that start at every 4-byte place of a 16-byte piece."""
     rng, d = np.random.default_rng(8), dev()
