@@ -96,20 +96,36 @@ __device__ __forceinline__ void each_id(const int32_t* ids, int R, int tid, F f)
     }
 }
 
-// offsets of all experts by one workgroup of NT threads
+// Ids that the lanes of a workgroup's first four waves hold, one each: compared as
+// they are, without counting in LDS (24 tokens of 7 slots @@)
+constexpr int kHeldIds = 256;
+
+// Workgroups that write the offsets beside those that move rows, NT threads each
+constexpr int offset_groups(int R, int E, int NT) { return R <= 64 ? E / NT + 1 : R <= kHeldIds ? E / 64 + 1 : 1; }
+
+// workgroup x of them
 template <int NT>
-__device__ __forceinline__ void write_offsets(const SortArgs& a) {
+__device__ __forceinline__ void write_offsets(const SortArgs& a, int x) {
     constexpr int kPer = kMaxE / NT;
     __shared__ int count[kMaxE];
     __shared__ int s_scan[NT / 64];
-    if (a.R <= 64) {
-        const int lane = threadIdx.x & 63;
-        const int id = lane < a.R ? a.ids[lane] : -1;
-        for (int e = threadIdx.x; e <= a.E; e += NT) {
-            int n = 0;
-            for (int i = 0; i < a.R; ++i) n += uint32_t(__builtin_amdgcn_readlane(id, i)) < uint32_t(e) ? 1 : 0;
-            a.offsets[e] = n;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (a.R <= kHeldIds) {
+        // R <= 64: an expert a thread, every wave over all ids; else 64 experts, a
+        // quarter of the ids a wave
+        const bool all = a.R <= 64;
+        const int i0 = all ? 0 : 64 * wv, e = all ? x * NT + threadIdx.x : 64 * x + lane;
+        const int here = min(a.R - i0, 64);                // below 1: no ids for this wave
+        const int id = lane < here ? a.ids[i0 + lane] : -1;
+        int n = 0;
+        for (int i = 0; i < here; ++i) n += uint32_t(__builtin_amdgcn_readlane(id, i)) < uint32_t(e) ? 1 : 0;
+        if (!all) {
+            if (wv < kHeldIds / 64) count[threadIdx.x] = n;
+            __syncthreads();
+            if (wv > 0) return;
+            for (int w = 1; w < kHeldIds / 64; ++w) n += count[64 * w + lane];
         }
+        if (e <= a.E) a.offsets[e] = n;
         return;
     }
     for (int e = threadIdx.x; e < kMaxE; e += NT) count[e] = 0;
@@ -131,18 +147,26 @@ __device__ __forceinline__ void write_offsets(const SortArgs& a) {
     if (a.E == kMaxE && threadIdx.x == NT - 1) a.offsets[kMaxE] = at;
 }
 
-// positions of token t's slots into pos[topk] (set to 0 before, with a barrier),
-// eight slots at a time, every wave counting over its share of the ids
+// positions of token t's slots into pos[topk] (set to 0 before, with a barrier);
+// few ids: a slot a wave; else eight slots at a time, every wave counting over its
+// share of the ids
 template <int NT>
 __device__ __forceinline__ void find_positions(const SortArgs& a, int t, int* pos) {
     constexpr int kAt = 8;
     const int lane = threadIdx.x & 63, own = t * a.topk;
-    if (a.R <= 64) {                                       // an id a lane: every wave by itself
-        const int id = lane < a.R ? a.ids[lane] : -1;
-        for (int j = 0; j < a.topk; ++j) {
-            const uint32_t e = uint32_t(__builtin_amdgcn_readlane(id, own + j));
-            const int n = __popcll(__ballot(uint32_t(id) < e + (lane < own + j ? 1u : 0u)));
-            if (lane == j) pos[j] = e < uint32_t(a.E) ? n : -1;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (a.R <= kHeldIds) {
+        int id[kHeldIds / 64];
+        const int mine = lane < a.topk ? a.ids[own + lane] : -1;
+#pragma unroll
+        for (int q = 0; q < kHeldIds / 64; ++q) id[q] = 64 * q + lane < a.R ? a.ids[64 * q + lane] : -1;
+        for (int j = wv; j < a.topk; j += NT / 64) {
+            const uint32_t e = uint32_t(__builtin_amdgcn_readlane(mine, j));
+            int n = 0;
+#pragma unroll
+            for (int q = 0; q < kHeldIds / 64; ++q)
+                n += __popcll(__ballot(uint32_t(id[q]) < e + (64 * q + lane < own + j ? 1u : 0u)));
+            if (lane == 0) pos[j] = e < uint32_t(a.E) ? n : -1;
         }
         return;
     }
@@ -160,11 +184,13 @@ __device__ __forceinline__ void find_positions(const SortArgs& a, int t, int* po
 #pragma unroll
             for (int q = 0; q < kAt; ++q) n[q] += uint32_t(id) < e[q] + (i < own + j0 + q ? 1u : 0u) ? 1 : 0;
         });
+        int mine = 0;                                      // lane q: slot j0 + q
 #pragma unroll
         for (int q = 0; q < kAt; ++q) {
-            const int sum = wave_sum(n[q]);
-            if (lane == q && j0 + q < a.topk) atomicAdd(&pos[j0 + q], e[q] < uint32_t(a.E) ? sum : -1);
+            const int sum = e[q] < uint32_t(a.E) ? wave_sum(n[q]) : -1;
+            if (lane == q) mine = sum;
         }
+        if (lane < kAt && j0 + lane < a.topk) atomicAdd(&pos[j0 + lane], mine);
     }
 }
 
@@ -332,7 +358,7 @@ __device__ __forceinline__ void copy_scales(const SortArgs& a, int64_t token, co
 }
 
 // A token's row (kSortInt8) or a part of it by a workgroup.  kOne: the positions
-// are found here, and one more workgroup writes the offsets.
+// are found here, and further workgroups write the offsets.
 template <SortMode kMode, int NT, int CH, bool kOne>
 __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, int span) {
     __shared__ int pos[MOE_MAX_TOPK];
@@ -340,7 +366,8 @@ __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, in
     const int64_t wg = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
     const int64_t token = wg / parts;
     if (token >= a.T) {                                    // the whole workgroup alike
-        if (kOne && wg == int64_t(a.T) * parts) write_offsets<NT>(a);
+        const int64_t x = wg - int64_t(a.T) * parts;
+        if (kOne && x < offset_groups(a.R, a.E, NT)) write_offsets<NT>(a, int(x));
         return;
     }
     const int t = int(token), part = int(wg - token * parts);
@@ -529,7 +556,7 @@ hipError_t launch_move(const SortArgs& a, bool counted, hipStream_t s) {
     const int span = kMode == kSortInt8 ? a.units : ((a.units + parts - 1) / parts + 7) / 8 * 8;
     if (!counted && !few_ids(a, parts)) return launch_batch<kMode>(a, s);
     if (counted && a.units <= 64) return launch_narrow<kMode>(a, s);
-    const int64_t n = int64_t(a.T) * parts + (counted ? 0 : 1);
+    const int64_t n = int64_t(a.T) * parts + (counted ? 0 : offset_groups(a.R, a.E, NT));
     void (*kern)(SortArgs, int, int) =
         counted ? sort_move_kernel<kMode, NT, CH, false> : sort_move_kernel<kMode, NT, CH, true>;
     return start(kern, grid_of(n), NT, s, a, parts, span);
