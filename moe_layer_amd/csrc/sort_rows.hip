@@ -96,35 +96,42 @@ __device__ __forceinline__ void each_id(const int32_t* ids, int R, int tid, F f)
     }
 }
 
-// Ids that the lanes of a workgroup's first four waves hold, one each: compared as
-// they are, without counting in LDS (24 tokens of 7 slots @@)
-constexpr int kHeldIds = 256;
+// Ids up to which a wave holds them all, for the positions of a token's slots, and
+// workgroups of 16 experts each compare them, for the offsets; more are counted in LDS
+// (us in a graph, 8 of 256 experts, to int8, held / counted: 16 x 4096 3.6 / 4.9, 64 x
+// 4096 3.9 / 5.2, 128 x 4096 4.4 / 4.9).
+constexpr int kHeldIds = 1024;
 
-// Workgroups that write the offsets beside those that move rows, NT threads each
-constexpr int offset_groups(int R, int E, int NT) { return R <= 64 ? E / NT + 1 : R <= kHeldIds ? E / 64 + 1 : 1; }
+// Workgroups that write the offsets beside those that move rows
+constexpr int offset_groups(int R, int E) { return R <= kHeldIds ? E / 16 + 1 : 1; }
 
 // workgroup x of them
 template <int NT>
 __device__ __forceinline__ void write_offsets(const SortArgs& a, int x) {
     constexpr int kPer = kMaxE / NT;
-    __shared__ int count[kMaxE];
+    __shared__ __attribute__((aligned(16))) int count[kMaxE];
     __shared__ int s_scan[NT / 64];
-    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (a.R <= kHeldIds) {
-        // R <= 64: an expert a thread, every wave over all ids; else 64 experts, a
-        // quarter of the ids a wave
-        const bool all = a.R <= 64;
-        const int i0 = all ? 0 : 64 * wv, e = all ? x * NT + threadIdx.x : 64 * x + lane;
-        const int here = min(a.R - i0, 64);                // below 1: no ids for this wave
-        const int id = lane < here ? a.ids[i0 + lane] : -1;
+        // 16 experts, one a lane, and NT / 16 parts of the ids
+        static_assert(kHeldIds <= kMaxE, "ids in count");
+        const int e = 16 * x + (threadIdx.x & 15), part = threadIdx.x >> 4;
+        const int quads = (a.R + 3) >> 2;
+        for (int i = threadIdx.x; i < 4 * quads; i += NT) count[i] = i < a.R ? a.ids[i] : -1;
+        __syncthreads();
         int n = 0;
-        for (int i = 0; i < here; ++i) n += uint32_t(__builtin_amdgcn_readlane(id, i)) < uint32_t(e) ? 1 : 0;
-        if (!all) {
-            if (wv < kHeldIds / 64) count[threadIdx.x] = n;
-            __syncthreads();
-            if (wv > 0) return;
-            for (int w = 1; w < kHeldIds / 64; ++w) n += count[64 * w + lane];
+        for (int q = part; q < quads; q += NT / 16) {
+            const i32x4 v = *reinterpret_cast<const i32x4*>(count + 4 * q);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) n += uint32_t(v[w]) < uint32_t(e) ? 1 : 0;
         }
+        n += __shfl_xor(n, 16);
+        n += __shfl_xor(n, 32);
+        __syncthreads();
+        const int lane = threadIdx.x & 63;
+        if (lane < 16) count[(threadIdx.x >> 6) * 16 + lane] = n;
+        __syncthreads();
+        if (threadIdx.x >= 16) return;
+        for (int w = 1; w < NT / 64; ++w) n += count[16 * w + lane];
         if (e <= a.E) a.offsets[e] = n;
         return;
     }
@@ -147,29 +154,35 @@ __device__ __forceinline__ void write_offsets(const SortArgs& a, int x) {
     if (a.E == kMaxE && threadIdx.x == NT - 1) a.offsets[kMaxE] = at;
 }
 
-// positions of token t's slots into pos[topk] (set to 0 before, with a barrier);
-// few ids: a slot a wave; else eight slots at a time, every wave counting over its
-// share of the ids
+// positions of token t's slots into pos[topk], a slot a wave, which holds all ids, Q a
+// lane (16 a lane for any number of ids: 16 x 4096 4.1 us, not 3.6)
+template <int NT, int Q>
+__device__ __forceinline__ void compare_held(const SortArgs& a, int t, int* pos) {
+    const int lane = threadIdx.x & 63, own = t * a.topk;
+    const int mine = lane < a.topk ? a.ids[own + lane] : -1;
+    int id[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) id[q] = 64 * q + lane < a.R ? a.ids[64 * q + lane] : -1;
+    for (int j = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); j < a.topk; j += NT / 64) {
+        const uint32_t e = uint32_t(__builtin_amdgcn_readlane(mine, j));
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            n += __popcll(__ballot(uint32_t(id[q]) < e + (64 * q + lane < own + j ? 1u : 0u)));
+        if (lane == 0) pos[j] = e < uint32_t(a.E) ? n : -1;
+    }
+}
+
+// positions of token t's slots into pos[topk] (set to 0 before, with a barrier); of
+// many ids eight slots at a time, every wave counting over its share of the ids
 template <int NT>
 __device__ __forceinline__ void find_positions(const SortArgs& a, int t, int* pos) {
     constexpr int kAt = 8;
     const int lane = threadIdx.x & 63, own = t * a.topk;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (a.R <= kHeldIds) {
-        int id[kHeldIds / 64];
-        const int mine = lane < a.topk ? a.ids[own + lane] : -1;
-#pragma unroll
-        for (int q = 0; q < kHeldIds / 64; ++q) id[q] = 64 * q + lane < a.R ? a.ids[64 * q + lane] : -1;
-        for (int j = wv; j < a.topk; j += NT / 64) {
-            const uint32_t e = uint32_t(__builtin_amdgcn_readlane(mine, j));
-            int n = 0;
-#pragma unroll
-            for (int q = 0; q < kHeldIds / 64; ++q)
-                n += __popcll(__ballot(uint32_t(id[q]) < e + (64 * q + lane < own + j ? 1u : 0u)));
-            if (lane == 0) pos[j] = e < uint32_t(a.E) ? n : -1;
-        }
-        return;
-    }
+    if (a.R <= 64) return compare_held<NT, 1>(a, t, pos);
+    if (a.R <= 256) return compare_held<NT, 4>(a, t, pos);
+    if (a.R <= 512) return compare_held<NT, 8>(a, t, pos);
+    if (a.R <= kHeldIds) return compare_held<NT, kHeldIds / 64>(a, t, pos);
     for (int j0 = 0; j0 < a.topk; j0 += kAt) {
         uint32_t e[kAt];
         int n[kAt];
@@ -367,7 +380,7 @@ __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, in
     const int64_t token = wg / parts;
     if (token >= a.T) {                                    // the whole workgroup alike
         const int64_t x = wg - int64_t(a.T) * parts;
-        if (kOne && x < offset_groups(a.R, a.E, NT)) write_offsets<NT>(a, int(x));
+        if (kOne && x < offset_groups(a.R, a.E)) write_offsets<NT>(a, int(x));
         return;
     }
     const int t = int(token), part = int(wg - token * parts);
@@ -534,7 +547,7 @@ hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
 
 // Whether few ids are read so few times that every workgroup may compare them all
 // (sort_move_kernel<.., true>): ids read in all, us in that form / in the batch
-// form: 512 tokens of 4096 to 8 experts, to int8 (2.0 M) 8.8 / 9.2, 256 of 7168 in
+// form: 512 tokens of 4096 to 8 experts, to int8 (2.0 M) 8.3 / 9.2, 256 of 7168 in
 // four parts (2.0 M) 9.5 / 11.5, 300 (2.8 M) 11.3 / 12.0; 600 to int8 (2.8 M) 11.6 /
 // 9.6, 700 (3.7 M) 12.4 / 10.1, 1031 (8.5 M) 19.3 / 12.7.  Few tokens do not fill the
 // batch form's waves.
@@ -556,7 +569,7 @@ hipError_t launch_move(const SortArgs& a, bool counted, hipStream_t s) {
     const int span = kMode == kSortInt8 ? a.units : ((a.units + parts - 1) / parts + 7) / 8 * 8;
     if (!counted && !few_ids(a, parts)) return launch_batch<kMode>(a, s);
     if (counted && a.units <= 64) return launch_narrow<kMode>(a, s);
-    const int64_t n = int64_t(a.T) * parts + (counted ? 0 : offset_groups(a.R, a.E, NT));
+    const int64_t n = int64_t(a.T) * parts + (counted ? 0 : offset_groups(a.R, a.E));
     void (*kern)(SortArgs, int, int) =
         counted ? sort_move_kernel<kMode, NT, CH, false> : sort_move_kernel<kMode, NT, CH, true>;
     return start(kern, grid_of(n), NT, s, a, parts, span);
