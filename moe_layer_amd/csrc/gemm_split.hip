@@ -41,9 +41,11 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
     // load before each LDS read
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
     const int64_t item = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
-    const int slot = int(item / ntiles), tile = int(item - int64_t(slot) * ntiles);
+    // (a 64-bit division is a long one)
+    const int slot = gridDim.y == 1 ? int(blockIdx.x / uint32_t(ntiles)) : int(item / ntiles);
+    const int tile = int(item - int64_t(slot) * ntiles);
     int e, row0, row1;
-    if (slot >= slots || !find_block<BT>(g, slot, e, row0, row1)) return;   // the whole workgroup alike
+    if (slot >= slots || !RowBlocks<BT>(g).find(g, slot, e, row0, row1)) return;   // the whole workgroup alike
 
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -628,16 +628,18 @@ __device__ __forceinline__ void tile_product_pair(const RowsGemmArgs& g, lds_t* 
 template <int BW, int BT>
 __device__ __forceinline__ bool find_tile(const RowsGemmArgs& g, int ntiles, int band, int& e, int& row0, int& row1,
                                           int& n0) {
-    const int slots = count_blocks<BT>(g);
+    const RowBlocks<BT> blocks(g);
+    const int64_t total = int64_t(blocks.total) * ntiles;
     int64_t item;
-    if (!xcd_item(int64_t(slots) * ntiles, item)) return false;   // the whole workgroup alike
-    const int64_t per_band = int64_t(band) * slots;
-    const int b = int(item / per_band);
+    if (!xcd_item(total, item)) return false;                // the whole workgroup alike
+    const bool small = total <= INT32_MAX;                   // a 64-bit division is a long one
+    const int64_t per_band = int64_t(band) * blocks.total;
+    const int b = small ? int(uint32_t(item) / uint32_t(per_band)) : int(item / per_band);
     const int64_t in = item - b * per_band;
     const int wide = min(band, ntiles - b * band);
-    const int slot = int(in / wide);
-    n0 = (b * band + int(in % wide)) * BW;
-    return find_block<BT>(g, slot, e, row0, row1);
+    const int slot = small ? int(uint32_t(in) / uint32_t(wide)) : int(in / wide);
+    n0 = (b * band + int(in - int64_t(slot) * wide)) * BW;
+    return blocks.find(g, slot, e, row0, row1);
 }
 
 template <bool NTW>

@@ -211,6 +211,30 @@ def test_grouped_gemm_int8(sizes, head, tail, N, K):
     assert same_bits(again, out)
 
 
+@pytest.mark.parametrize("E", [1, 3, 4, 5, 63, 64, 65, 255, 256, 257, 260, 1000, 1024])
+@pytest.mark.parametrize("N,K,per", [(40, 64, 2), (300, 144, 40)])
+def test_grouped_gemm_int8_numbers_of_groups(E, N, K, per):
+    """Groups of 0 to 2 per rows, empty ones first, in between and last, in small and
+    large tiles, for every number of groups at which the search for a block changes."""
+    rng, d, g = np.random.default_rng(E + K), dev(), torch.Generator(device=dev()).manual_seed(E)
+    sizes = rng.integers(0, 2 * per + 1, E) * (rng.random(E) < 0.7)
+    sizes[E // 2] += 1
+    sizes[-1] = 0 if E > 1 else 3
+    off = np.concatenate([[3], 3 + np.cumsum(sizes)]).astype(np.int32)
+    rows = int(off[-1]) + 5
+    a = torch.randint(-128, 128, (rows, K), generator=g, device=d, dtype=torch.int8)
+    w = torch.randint(-128, 128, (E, N, K), generator=g, device=d, dtype=torch.int8)
+    sa, sw = torch.rand(rows, generator=g, device=d), torch.rand(E, N, generator=g, device=d)
+    out = torch.full((rows, N), 5.0, dtype=torch.bfloat16, device=d)
+    ops.moe_grouped_gemm(a, w, torch.from_numpy(off).to(d), sa, sw, out=out)
+    assert (out[:3] == 5.0).all() and (out[rows - 5:] == 5.0).all()
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if hi > lo:
+            S = (a[lo:hi].double() @ w[e].double().t()).float()
+            assert torch.equal(out[lo:hi], ((S * sa[lo:hi, None]) * sw[e]).bfloat16()), e
+
+
 @pytest.mark.parametrize("off", [[-5, 3, 7, 400], [10, 4, 90, 60], [0, 1000, 1000, 2000], [120, 120, 120, 120]])
 def test_grouped_int8_bad_offsets_stay_in_bounds(off):
     rows, E, N, K = 100, 3, 200, 240
