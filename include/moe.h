@@ -548,8 +548,8 @@ MOE_API int moe_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* w
  * block padding):
  *   out[r, n] = bf16(sum_k a[r, k] w[e, n, k]) for offsets[e] <= r < offsets[e+1]
  * in bf16 (fp32 sums), in fp8 with moe_gemm_fp8's scales and arithmetic, or in
- * 8-bit integers with moe_gemm_int8's.  Rows outside every group (before offsets[0], from offsets[E]
- * on) are neither read nor written; groups may be empty.
+ * 8-bit integers with moe_gemm_int8's.  Rows outside every group (before
+ * offsets[0], from offsets[E] on) are neither read nor written; groups may be empty.
  *
  *   a        device, bf16, E4M3FN or int8 [rows, K]
  *   a_scale  device, fp32 [rows, K / 128] (FP8_E4M3) or [rows] (INT8), else NULL
@@ -649,8 +649,9 @@ MOE_API int moe_combine_rows(const void* rows, const int32_t* inv, const float* 
  *   grad_rows[inv[t, j]] = bf16(weights[t, j] grad_out[t])
  *   grad_weights[t, j] = sum_h grad_out[t, h] rows[inv[t, j], h]   (fp32)
  * Slots whose inv lies outside [0, num_rows) have no row and grad_weights 0.
- * Rows that no slot has are not written; a row that two slots have (moe_sort_rows
- * makes no such inv) gets the gradient of one of them.
+ * Rows that no slot has are not written.  A row has one slot, as moe_sort_rows
+ * makes them: of one that several name, each value of grad_rows is one of theirs,
+ * unspecified which, and not their sum.
  *
  *   grad_out      device, bf16 [T, cols]
  *   rows          device, bf16 [num_rows, cols]; NULL where grad_weights is NULL

@@ -12,7 +12,10 @@
 //               block adds the counts before its own and ranks its slots
 //               (sort_place_kernel), then the rows are moved: three launches, for
 //               more ids than every workgroup should read.
-// A row is read once and stored topk times.
+// A row is read once and stored topk times: large batches are bound by those bytes
+// (8192 x 7168 bf16 to 8 of 128 experts 212 us, 5.0 TB/s, 10 of them to find the
+// positions), single tokens by the launch (kernel 2.8 us), batches in between by the
+// look at all ids in front (1031 x 4096 to int8 13.0 us, 8.3 of them bytes).
 #include "dev_align.h"
 #include "moe.h"
 #include "sorted.h"

@@ -588,6 +588,7 @@ def moe_combine_rows_bwd(grad_out: torch.Tensor, inv: torch.Tensor, rows=None, w
     grad_rows[inv[t, j]] = weights[t, j] grad_out[t], and where ``rows`` is given
     fp32 grad_weights[t, j] = grad_out[t] . rows[inv[t, j]].  grad_rows has as
     many rows as ``rows`` (without them T * topk when allocated here); rows that
-    no slot has keep what they held (uninitialised when allocated here).
+    no slot has keep what they held (uninitialised when allocated here), and no
+    row may be named by two slots (moe_sort_rows names none twice).
     Returns (grad_rows, grad_weights or None)."""
     return _call("combine_rows_bwd", grad_out, inv, rows, weights, grad_rows, grad_weights)
