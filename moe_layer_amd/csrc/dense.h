@@ -70,6 +70,17 @@ __device__ __forceinline__ float quant8(const i32x4& w, uint32_t& lo, uint32_t& 
     return s;
 }
 
+// inclusive sum over the wave's lanes, in lane order
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast 31 into rows 2 and 3
+    return v;
+}
+
 // Launch one kernel with its arguments (what <<<>>> does, in one runtime call
 // instead of three; these launches stand between kernels of a few us).
 template <typename... P, typename... A>

@@ -110,17 +110,6 @@ __device__ __forceinline__ int count_blocks(const RowsGemmArgs& g) {
     return __builtin_amdgcn_readfirstlane(n);
 }
 
-// inclusive sum over the wave's lanes, in lane order
-__device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15 into rows 1 and 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast 31 into rows 2 and 3
-    return v;
-}
-
 // count_blocks and find_block for the same BM with one look at the offsets: up to
 // kHeldGroups groups stay in the wave's registers, four a lane.  Every workgroup starts
 // with this and loads nothing before (188 rows in 256 int8 groups of 440 x 368 10.2 ->

@@ -52,51 +52,70 @@ __device__ __forceinline__ int wave_sum(int v) {
     return int(b[0] + b[1]);
 }
 
-// Exclusive scan over the workgroup's threads of v[0 .. PER) in thread order;
+// Exclusive scan over the workgroup's W waves' threads of v[0 .. PER) in thread order;
 // s: one int per wave.  Returns this thread's start.
-template <int PER>
+template <int W, int PER>
 __device__ __forceinline__ int scan_start(const int (&v)[PER], int* s) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) mine += v[i];
-    int sum = mine;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const int up = __shfl_up(sum, m);
-        if (lane >= m) sum += up;
-    }
+    const int sum = wave_scan(mine);
     if (lane == 63) s[w] = sum;
     __syncthreads();
-    int before = 0;
-    for (int i = 0; i < w; ++i) before += s[i];
-    return before + sum - mine;
+    int before = sum - mine;
+#pragma unroll
+    for (int i = 0; i < W; ++i) before += i < w ? s[i] : 0;
+    return before;
 }
 
 // f(i, ids[i]) for every i below R, by NT threads: 16-byte loads, kFlight of them in
-// flight, and single ones in front of the first 16-byte border and behind the last
-template <int NT, int kFlight, typename F>
-__device__ __forceinline__ void each_id(const int32_t* ids, int R, int tid, F f) {
-    const int head = min(R, int(-(reinterpret_cast<uintptr_t>(ids) >> 2) & 3)), quads = (R - head) >> 2;
-    const i32x4* four = reinterpret_cast<const i32x4*>(ids + head);
-    for (int q0 = 0; q0 < quads; q0 += NT * kFlight) {
-        i32x4 v[kFlight];
+// flight, and single ones in front of the first 16-byte border and behind the last.
+// load_first() may precede each() by other work.
+template <int NT, int kFlight>
+struct EachId {
+    const int32_t* ids;
+    const i32x4* four;
+    int R, head, quads;
+    i32x4 v[kFlight];
+
+    __device__ __forceinline__ EachId(const int32_t* p, int n) : ids(p), R(n) {
+        head = min(R, int(-(reinterpret_cast<uintptr_t>(ids) >> 2) & 3));
+        quads = (R - head) >> 2;
+        four = reinterpret_cast<const i32x4*>(ids + head);
+    }
+    __device__ __forceinline__ void load(int q0) {
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) v[u] = four[min(q0 + u * NT + tid, quads - 1)];
+        for (int u = 0; u < kFlight; ++u) v[u] = four[min(q0 + u * NT + int(threadIdx.x), quads - 1)];
+    }
+    __device__ __forceinline__ void load_first() {
+        if (quads > 0) load(0);
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(F f) {
+        for (int q0 = 0; q0 < quads; q0 += NT * kFlight) {
+            if (q0 > 0) load(q0);
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            const int q = q0 + u * NT + tid;
-            if (q < quads) {
+            for (int u = 0; u < kFlight; ++u) {
+                const int q = q0 + u * NT + threadIdx.x;
+                if (q < quads) {
 #pragma unroll
-                for (int w = 0; w < 4; ++w) f(head + 4 * q + w, v[u][w]);
+                    for (int w = 0; w < 4; ++w) f(head + 4 * q + w, v[u][w]);
+                }
             }
         }
+        const int rest = R - 4 * quads;                    // in front and behind, 6 at most
+        if (int(threadIdx.x) < rest) {
+            const int i = int(threadIdx.x) < head ? int(threadIdx.x) : int(threadIdx.x) + 4 * quads;
+            f(i, ids[i]);
+        }
     }
-    const int rest = R - 4 * quads;                        // in front and behind, 6 at most
-    if (tid < rest) {
-        const int i = tid < head ? tid : tid + 4 * quads;
-        f(i, ids[i]);
-    }
+};
+template <int NT, int kFlight, typename F>
+__device__ __forceinline__ void each_id(const int32_t* p, int n, F f) {
+    EachId<NT, kFlight> ids(p, n);
+    ids.load_first();
+    ids.each(f);
 }
 
 // Ids up to which a wave holds them all, for the positions of a token's slots, and
@@ -140,14 +159,14 @@ __device__ __forceinline__ void write_offsets(const SortArgs& a, int x) {
     }
     for (int e = threadIdx.x; e < kMaxE; e += NT) count[e] = 0;
     __syncthreads();
-    each_id<NT, 2>(a.ids, a.R, threadIdx.x, [&](int, int id) {
+    each_id<NT, 2>(a.ids, a.R, [&](int, int id) {
         if (uint32_t(id) < uint32_t(a.E)) atomicAdd(&count[id], 1);
     });
     __syncthreads();
     int n[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) n[i] = count[threadIdx.x * kPer + i];
-    int at = scan_start(n, s_scan);
+    int at = scan_start<NT / 64>(n, s_scan);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;
@@ -196,7 +215,7 @@ __device__ __forceinline__ void find_positions(const SortArgs& a, int t, int* po
         }
         // a slot before counts where its expert is not above, one from the slot on
         // where it is below; an unrouted id is above every expert
-        each_id<NT, 2>(a.ids, a.R, threadIdx.x, [&](int i, int id) {
+        each_id<NT, 2>(a.ids, a.R, [&](int i, int id) {
 #pragma unroll
             for (int q = 0; q < kAt; ++q) n[q] += uint32_t(id) < e[q] + (i < own + j0 + q ? 1u : 0u) ? 1 : 0;
         });
@@ -287,7 +306,7 @@ __global__ __launch_bounds__(kPlaceThreads) void sort_place_kernel(SortArgs a, i
     int n[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) n[i] = total[threadIdx.x * kPer + i];
-    int at = scan_start(n, s_scan);
+    int at = scan_start<kWaves>(n, s_scan);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;
@@ -446,7 +465,7 @@ template <SortMode kMode, int CH, int L>
 __global__ __launch_bounds__(kBatchThreads) void sort_batch_kernel(SortArgs a, int per, int rep, int span) {
     constexpr int NT = kBatchThreads, kPer = kMaxE / NT, kTeams = NT / L, kWaves = L / 64;
     static_assert(L <= 64 ? CH == 1 : L % 64 == 0, "lanes");
-    __shared__ int count[2 * kMaxE];        // [before, from][E][1 << rep], then a slot's next position in each expert
+    __shared__ __attribute__((aligned(16))) int count[2 * kMaxE];   // [before, from][E][1 << rep], then a slot's next position in each expert
     __shared__ int pos[kBatchSlots];
     __shared__ int s_scan[NT / 64];
     __shared__ uint32_t s_max[2][NT / 64];
@@ -462,29 +481,40 @@ __global__ __launch_bounds__(kBatchThreads) void sort_batch_kernel(SortArgs a, i
         for (int c = 0; c < CH; ++c) p[c].load(a.x + t * row_bytes, min(u + at_row + L * c, u1 - 1));
         if (kMode == kSortCopy && u == 0) scale = first_scale(a, t, at_row);
     };
+    EachId<NT, 8> ids(a.ids, a.R);
+    ids.load_first();
+    const int own = first * a.topk, copy = lane & ((1 << rep) - 1);
+    const int own_id = own + lane < last * a.topk ? a.ids[own + lane] : -1;
     load(min(first + team, a.T - 1), u0);
 
     for (int i = threadIdx.x; i < 2 * kMaxE; i += NT) count[i] = 0;
     __syncthreads();
-    const int own = first * a.topk, copy = lane & ((1 << rep) - 1);
-    const int own_id = own + lane < last * a.topk ? a.ids[own + lane] : -1;
-    each_id<NT, 8>(a.ids, a.R, threadIdx.x, [&](int i, int id) {
+    ids.each([&](int i, int id) {
         if (uint32_t(id) < uint32_t(a.E)) atomicAdd(&count[((i >= own ? a.E : 0) + id << rep) + copy], 1);
     });
     __syncthreads();
     int before[kPer], n[kPer];
+    auto add_copies = [&](auto copies) {
+        constexpr int C = decltype(copies)::value;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * kPer + i;
-        before[i] = n[i] = 0;
-        if (e < a.E)
-            for (int r = 0; r < 1 << rep; ++r) {
-                before[i] += count[(e << rep) + r];
-                n[i] += count[(a.E + e << rep) + r];
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            before[i] = n[i] = 0;
+            if (e < a.E) {
+#pragma unroll
+                for (int r = 0; r < C; ++r) {
+                    before[i] += count[e * C + r];
+                    n[i] += count[(a.E + e) * C + r];
+                }
+                n[i] += before[i];
             }
-        n[i] += before[i];
-    }
-    int at = scan_start(n, s_scan);                        // (a barrier behind every read of count)
+        }
+    };
+    if (rep == 0) add_copies(std::integral_constant<int, 1>());
+    else if (rep == 1) add_copies(std::integral_constant<int, 2>());
+    else if (rep == 2) add_copies(std::integral_constant<int, 4>());
+    else add_copies(std::integral_constant<int, 8>());
+    int at = scan_start<NT / 64>(n, s_scan);               // (a barrier behind every read of count)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;
