@@ -15,7 +15,7 @@
 // A row is read once and stored topk times: large batches are bound by those bytes
 // (8192 x 7168 bf16 to 8 of 128 experts 212 us, 5.0 TB/s, 10 of them to find the
 // positions), single tokens by the launch (kernel 2.8 us), batches in between by the
-// look at all ids in front (1031 x 4096 to int8 13.0 us, 8.3 of them bytes).
+// look at all ids in front (1031 x 4096 to int8 11.3 us, 8.3 of them bytes).
 #include "dev_align.h"
 #include "moe.h"
 #include "sorted.h"
@@ -26,10 +26,10 @@ namespace {
 
 constexpr int kThreads = 256, kPlaceThreads = 1024;
 // Slots up to which every workgroup of the batch form counts all ids.  us, batch /
-// counted, 256 experts: 4000 tokens to 8, 4096 columns to int8 32.6 / 33.8, bf16 54.0 /
-// 54.9, 1024 columns 19.1 / 20.9; 6000 (48000 slots) 47.2 / 46.0, 98.5 / 100, 27.7 / 27.3;
-// 8000 74.7 / 69.7, 133 / 125, 35.1 / 33.4.
-constexpr int kBatchMostSlots = 32768;
+// counted, 8 of 256 experts: 4000 tokens of 4096 to int8 30.3 / 33.2, bf16 50.2 / 54.2, of
+// 1024 18.2 / 20.4; 6000 (48000 slots) 44.9 / 45.4, 95.2 / 98.2, 26.3 / 27.2; 8000 71.7 /
+// 69.7, 127.8 / 126.7, 34.3 / 33.2.
+constexpr int kBatchMostSlots = 49152;
 constexpr int kMostBlocks = 256;
 constexpr int kBatchThreads = 512;
 // tokens of a workgroup of the batch form: about 512 workgroups
@@ -460,12 +460,14 @@ __global__ __launch_bounds__(kThreads) void sort_narrow_kernel(SortArgs a) {
 // `span` pieces of it.  The workgroup counts all ids by expert, those before its own
 // slots apart, in `1 << rep` copies (lanes of one expert add to different ones), and
 // ranks its own slots; its first rows are on their way meanwhile.  Two waves to a long
-// row: 1031 x 4096 to int8 12.7 us, one 14.5, four 12.8; 4000 tokens 32.7 / 36.8 / 31.9.
+// row: 1031 x 4096 to int8 12.7 us, one 14.5, four 12.8; 4000 tokens 32.7 / 36.8 / 31.9
+// (11.3 and 30.3 since the ids are on their way before the counters are cleared).
 template <SortMode kMode, int CH, int L>
 __global__ __launch_bounds__(kBatchThreads) void sort_batch_kernel(SortArgs a, int per, int rep, int span) {
     constexpr int NT = kBatchThreads, kPer = kMaxE / NT, kTeams = NT / L, kWaves = L / 64;
     static_assert(L <= 64 ? CH == 1 : L % 64 == 0, "lanes");
-    __shared__ __attribute__((aligned(16))) int count[2 * kMaxE];   // [before, from][E][1 << rep], then a slot's next position in each expert
+    // [before, from][E][1 << rep], then a slot's next position in each expert
+    __shared__ __attribute__((aligned(16))) int count[2 * kMaxE];
     __shared__ int pos[kBatchSlots];
     __shared__ int s_scan[NT / 64];
     __shared__ uint32_t s_max[2][NT / 64];
@@ -580,10 +582,9 @@ hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
 
 // Whether few ids are read so few times that every workgroup may compare them all
 // (sort_move_kernel<.., true>): ids read in all, us in that form / in the batch
-// form: 512 tokens of 4096 to 8 experts, to int8 (2.0 M) 8.3 / 9.2, 256 of 7168 in
-// four parts (2.0 M) 9.5 / 11.5, 300 (2.8 M) 11.3 / 12.0; 600 to int8 (2.8 M) 11.6 /
-// 9.6, 700 (3.7 M) 12.4 / 10.1, 1031 (8.5 M) 19.3 / 12.7.  Few tokens do not fill the
-// batch form's waves.
+// form: 8 experts, 512 tokens of 4096 to int8 (2.0 M) 8.2 / 8.5, 300 of 7168 in four
+// parts (2.8 M) 10.8 / 11.2; 600 to int8 (2.8 M) 10.8 / 8.9, 700 (3.7 M) 11.8 / 9.2, 400
+// of 7168 (4.9 M) 13.9 / 12.4.  Few tokens do not fill the batch form's waves.
 bool few_ids(const SortArgs& a, int parts) { return a.T <= 256 || int64_t(a.T) * parts * a.R <= 5 << 19; }
 
 template <SortMode kMode>

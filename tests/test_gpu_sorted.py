@@ -149,7 +149,7 @@ NARROW = {("bf16", None): (8, 64, 72, 256, 504, 512, 520), ("bf16", "int8"): (16
 
 
 @pytest.mark.parametrize("kind,quant", KINDS)
-@pytest.mark.parametrize("T,k", [(2501, 3), (6260, 4), (8193, 4), (11001, 3)])
+@pytest.mark.parametrize("T,k", [(2501, 3), (6260, 4), (13001, 4), (17001, 3)])
 def test_sort_rows_narrow(T, k, kind, quant):
     """Rows that a part of a wave takes, in the two forms for many ids; the last
     tokens leave lanes of a wave without one."""

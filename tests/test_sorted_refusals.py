@@ -37,9 +37,9 @@ def sort(**kw):
     (dict(rt=INT8, rs=C.c_void_p(FAKE + 6 * GAP + 2)), BAD),
     (dict(rows=P(0)), BAD), (dict(rows=C.c_void_p(FAKE + 4 * 512 - 16)), BAD), (dict(inv=P(1)), BAD),
     (dict(off=P(4)), BAD), (dict(rt=INT8, rs=P(3)), BAD), (dict(rows=P(4)), BAD),
-    (dict(T=20000), WS), (dict(T=20000, scratch=P(7), room=40 * 8 * 4 - 1), WS),
-    (dict(T=20000, scratch=C.c_void_p(FAKE + 7 * GAP + 2), room=1 << 20), WS),
-    (dict(T=20000, scratch=P(0), room=1 << 20), BAD), (dict(T=20000, scratch=P(4), room=1 << 20), BAD),
+    (dict(T=30000), WS), (dict(T=30000, scratch=P(7), room=59 * 8 * 4 - 1), WS),
+    (dict(T=30000, scratch=C.c_void_p(FAKE + 7 * GAP + 2), room=1 << 20), WS),
+    (dict(T=30000, scratch=P(0), room=1 << 20), BAD), (dict(T=30000, scratch=P(4), room=1 << 20), BAD),
 ])
 def test_sort_rows(kw, status):
     assert sort(**kw) == status
