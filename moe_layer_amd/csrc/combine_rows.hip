@@ -6,8 +6,8 @@
 // its weight's gradient is 0.
 //
 // Every row is read once and every output written once, so both are bound by bytes:
-// the combine of 8192 x 7168 and 8 slots 206 us, 5.1 TB/s, the rate of a large copy; the
-// gradient of 4096 x 4096 and 8 slots 118 us, 4.85 TB/s.  A thread has one piece of 16
+// the combine of 8192 x 7168 and 8 slots 179 us, 5.9 TB/s (a large copy 5.1); the
+// gradient of 4096 x 4096 and 8 slots 113 us, 5.05 TB/s.  A thread has one piece of 16
 // bytes of a token, which fills the CUs from a few tokens on, with the loads of eight
 // slots in flight; gathering by token needs no atomics and sums in slot order.
 #include "sorted.h"
@@ -45,7 +45,7 @@ struct Columns {
 
 // A thread makes 8 columns of a token.  kUniform: a wave's 512 columns are one
 // token's, whose positions and weights are then scalar loads.
-template <bool kUniform, bool kWeights>
+template <bool kUniform, bool kWeights, bool kPast>
 __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineArgs a, Columns n) {
     const uint32_t mine = blockIdx.x * uint32_t(kThreads) + threadIdx.x;
     if (mine >= n.total) return;
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineArgs a, C
             there[u] = j0 + u < a.topk && uint32_t(r) < uint32_t(a.num_rows);
             w[u] = kWeights ? weights[j] : 1.0f;
             v[u] = i32x4{0, 0, 0, 0};
-            if (there[u]) v[u] = *reinterpret_cast<const i32x4*>(a.rows + int64_t(r) * a.cols + h);
+            if (there[u]) v[u] = load16<kPast>(a.rows + int64_t(r) * a.cols + h);
         }
 #pragma unroll
         for (int u = 0; u < kSlots; ++u) {
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineArgs a, C
 
 // A token by W waves, which go over its columns in turn; a lane's part of every
 // slot's dot product stays in registers until the end.
-template <int W, bool kDots, bool kWeights>
+template <int W, bool kDots, bool kWeights, bool kPast>
 __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void combine_rows_bwd_kernel(CombineArgs a) {
     constexpr int NT = W <= 4 ? 256 : 64 * W, kTokens = NT / 64 / W;
     __shared__ float s_dot[NT / 64][kSlots];
@@ -115,12 +115,12 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void combine_rows_bwd_kernel
             dot[u] = 0.0f;
         }
         for (int i = tid; i < nvec; i += 64 * W) {
-            const i32x4 g = *reinterpret_cast<const i32x4*>(grad + i * 8);
+            const i32x4 g = load16<kPast>(grad + i * 8);
             i32x4 v[kSlots];
             if constexpr (kDots) {
 #pragma unroll
                 for (int u = 0; u < kSlots; ++u)
-                    if (r[u] >= 0) v[u] = *reinterpret_cast<const i32x4*>(a.rows + int64_t(r[u]) * a.cols + i * 8);
+                    if (r[u] >= 0) v[u] = load16<kPast>(a.rows + int64_t(r[u]) * a.cols + i * 8);
             }
 #pragma unroll
             for (int u = 0; u < kSlots; ++u) {
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 64 * W) void combine_rows_bwd_kernel
                     for (int q = 0; q < 4; ++q)
                         o[q] = int(pack_bf16(__fmul_rn(w[u], bf16_lo(g[q])), __fmul_rn(w[u], bf16_hi(g[q]))));
                 }
-                *reinterpret_cast<i32x4*>(a.grad_rows + int64_t(r[u]) * a.cols + i * 8) = o;
+                store16<kPast>(a.grad_rows + int64_t(r[u]) * a.cols + i * 8, o);
                 if constexpr (kDots) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -169,7 +169,9 @@ template <int W, bool kDots, bool kWeights>
 hipError_t launch_bwd(const CombineArgs& a, hipStream_t s) {
     constexpr int NT = W <= 4 ? 256 : 64 * W, kTokens = NT / 64 / W;
     const int64_t n = (int64_t(a.T) + kTokens - 1) / kTokens;
-    return start(combine_rows_bwd_kernel<W, kDots, kWeights>, grid_of(n), NT, s, a);
+    void (*kern)(CombineArgs) = a.past ? combine_rows_bwd_kernel<W, kDots, kWeights, true>
+                                       : combine_rows_bwd_kernel<W, kDots, kWeights, false>;
+    return start(kern, grid_of(n), NT, s, a);
 }
 
 // Columns up to which a wave takes a token (us, one wave / four: 2048 tokens of 256
@@ -185,6 +187,14 @@ hipError_t launch_bwd(const CombineArgs& a, hipStream_t s) {
     return launch_bwd<4, kDots, kWeights>(a, s);
 }
 
+// Whether there are more rows than stay in the last-level cache (us as they are / past
+// it: the combine of 224 MiB 39.4 / 46.5, 448 MiB 104 / 93, 896 MiB 206 / 178; its
+// gradient, rows read and written, of 224 MiB 105 / 102, 256 MiB 118 / 113, 896 MiB 405 /
+// 395.  The combine's output is left to the caches: 179 / 183)
+bool streamed(const CombineArgs& a) {
+    return std::min<int64_t>(int64_t(a.T) * a.topk, a.num_rows) * a.cols * 2 >= kLastCacheBytes;
+}
+
 }  // namespace
 
 hipError_t launch_combine_rows(const CombineArgs& all, hipStream_t s) {
@@ -197,9 +207,15 @@ hipError_t launch_combine_rows(const CombineArgs& all, hipStream_t s) {
     n.magic = uint32_t((uint64_t(1) << n.shift) / n.per_row + 1);
     const int most = int(std::min<int64_t>(a.T, INT32_MAX / int64_t(n.per_row)));
     const bool uniform = n.per_row % 64 == 0;
-    void (*kern)(CombineArgs, Columns) =
-        a.weights ? uniform ? combine_rows_kernel<true, true> : combine_rows_kernel<false, true>
-                  : uniform ? combine_rows_kernel<true, false> : combine_rows_kernel<false, false>;
+    a.past = streamed(a) && reads_past(a.rows, int64_t(a.cols) * 2);
+    void (*const kern)(CombineArgs, Columns) =
+        pick(uniform, [&](auto u) {
+            return pick(a.weights != nullptr, [&](auto w) {
+                return pick(a.past, [&](auto p) -> void (*)(CombineArgs, Columns) {
+                    return combine_rows_kernel<u.value, w.value, p.value>;
+                });
+            });
+        });
     for (int t0 = 0; t0 < all.T; t0 += std::min(most, all.T - t0)) {
         a.inv = all.inv + int64_t(t0) * a.topk;
         a.weights = all.weights ? all.weights + int64_t(t0) * a.topk : nullptr;
@@ -211,7 +227,9 @@ hipError_t launch_combine_rows(const CombineArgs& all, hipStream_t s) {
     return hipSuccess;
 }
 
-hipError_t launch_combine_rows_bwd(const CombineArgs& a, hipStream_t s) {
+hipError_t launch_combine_rows_bwd(const CombineArgs& all, hipStream_t s) {
+    CombineArgs a = all;
+    a.past = streamed(a) && whole_lines(a.grad_rows, int64_t(a.cols) * 2);
     if (a.grad_weights) return a.weights ? launch_bwd<true, true>(a, s) : launch_bwd<true, false>(a, s);
     return a.weights ? launch_bwd<false, true>(a, s) : launch_bwd<false, false>(a, s);
 }

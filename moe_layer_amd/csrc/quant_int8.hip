@@ -6,8 +6,8 @@
 // A row is held in the registers of L lanes, CH chunks of 8 columns each, so it is
 // read once; the maximum of the row's bf16 bits is joined through lane permutations
 // and, where several waves have a row, LDS.  Rows of up to 32 chunks share a wave (24265
-// x 80 gated 4.6 us, a wave to a row 11.6).  Many rows are bound by their bytes (5.1
-// TB/s, the rate of a large copy), few by the launch (3.6-4 us).
+// x 80 gated 4.6 us, a wave to a row 11.6).  Many rows are bound by their bytes
+// (32771 x 1536 gated 46.6 us, 5.4 TB/s), few by the launch (3.6-4 us).
 #include "moe.h"
 
 #include "dev_silu.h"
@@ -21,7 +21,7 @@ namespace {
 template <int L>
 constexpr int kThreads = L <= 256 ? 256 : L;
 
-template <int L, int CH, bool kGated, bool kClamp>
+template <int L, int CH, bool kGated, bool kClamp, bool kPast>
 __global__ __launch_bounds__(kThreads<L>) void quant_int8_kernel(Int8Args a) {
     constexpr int NT = kThreads<L>;
     __shared__ uint32_t s_max[NT / 64];
@@ -35,8 +35,8 @@ __global__ __launch_bounds__(kThreads<L>) void quant_int8_kernel(Int8Args a) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int i = min(tid + c * L, nvec - 1);     // behind the row: its last chunk again
-        v[c] = *reinterpret_cast<const i32x4*>(x + i * 8);
-        if constexpr (kGated) u[c] = *reinterpret_cast<const i32x4*>(x + a.cols + i * 8);
+        v[c] = load16<kPast>(x + i * 8);
+        if constexpr (kGated) u[c] = load16<kPast>(x + a.cols + i * 8);
     }
     uint32_t most = 0;
 #pragma unroll
@@ -78,7 +78,9 @@ hipError_t launch(const Int8Args& a, hipStream_t s) {
     auto go = [&](auto lanes, auto ch) {
         constexpr int L = decltype(lanes)::value, CH = decltype(ch)::value, kRows = kThreads<L> / L;
         const int64_t n = (int64_t(a.rows) + kRows - 1) / kRows;
-        return start(quant_int8_kernel<L, CH, kGated, kClamp>, grid_of(n), kThreads<L>, s, a);
+        void (*kern)(Int8Args) = a.past ? quant_int8_kernel<L, CH, kGated, kClamp, true>
+                                        : quant_int8_kernel<L, CH, kGated, kClamp, false>;
+        return start(kern, grid_of(n), kThreads<L>, s, a);
     };
     using std::integral_constant;
     const integral_constant<int, 1> one;
@@ -109,7 +111,13 @@ hipError_t launch(const Int8Args& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_quant_int8(const Int8Args& a, bool gated, hipStream_t s) {
+hipError_t launch_quant_int8(const Int8Args& all, bool gated, hipStream_t s) {
+    // three quarters of the cache, whose rest the codes take (us as they are / past, gated,
+    // and with a kernel that writes x in front: 96 MiB 22.7 / 23.4 (51 / 52), 192 MiB 39.8 /
+    // 41.9 (118 / 112), 256 MiB 62.7 / 55.1 (171 / 150), 384 MiB 96 / 81 (250 / 232))
+    Int8Args a = all;
+    const int64_t row_bytes = int64_t(a.cols) * (gated ? 4 : 2);
+    a.past = a.rows * row_bytes >= kLastCacheBytes / 4 * 3 && reads_past(a.x, row_bytes);
     if (!gated) return launch<false, false>(a, s);
     return a.limit > 0.0f ? launch<true, true>(a, s) : launch<true, false>(a, s);
 }

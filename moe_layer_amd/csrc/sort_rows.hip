@@ -13,7 +13,7 @@
 //               (sort_place_kernel), then the rows are moved: three launches, for
 //               more ids than every workgroup should read.
 // A row is read once and stored topk times: large batches are bound by those bytes
-// (8192 x 7168 bf16 to 8 of 128 experts 212 us, 5.0 TB/s, 10 of them to find the
+// (8192 x 7168 bf16 to 8 of 128 experts 187 us, 5.7 TB/s, 10 of them to find the
 // positions), single tokens by the launch (kernel 2.8 us), batches in between by the
 // look at all ids in front (1031 x 4096 to int8 11.3 us, 8.3 of them bytes).
 #include "dev_align.h"
@@ -346,7 +346,7 @@ struct Piece {
 // positions of the token's slots.  kSortInt8: bits is the row's largest magnitude;
 // kSortFp8: a lane's piece and its neighbours' make whole groups.  kWaves: a wave's
 // lanes have one token.
-template <SortMode kMode, int CH, bool kWaves = true>
+template <SortMode kMode, int CH, bool kWaves, bool kPast>
 __device__ __forceinline__ void store_pieces(const SortArgs& a, const Piece<kMode> (&p)[CH], const int* pos, int u0,
                                              int u1, int stride, uint32_t bits) {
     i32x4 out[CH];
@@ -371,7 +371,7 @@ __device__ __forceinline__ void store_pieces(const SortArgs& a, const Piece<kMod
         for (int c = 0; c < CH; ++c) {
             const int u = u0 + c * stride;
             if (u < u1) {
-                *reinterpret_cast<i32x4*>(to + int64_t(u) * 16) = out[c];
+                store16<kPast>(to + int64_t(u) * 16, out[c]);
                 if (kMode == kSortFp8 && (u & 7) == 0) a.row_scales[int64_t(at) * a.scales + (u >> 3)] = s[c];
             }
         }
@@ -394,7 +394,7 @@ __device__ __forceinline__ void copy_scales(const SortArgs& a, int64_t token, co
 
 // A token's row (kSortInt8) or a part of it by a workgroup.  kOne: the positions
 // are found here, and further workgroups write the offsets.
-template <SortMode kMode, int NT, int CH, bool kOne>
+template <SortMode kMode, int NT, int CH, bool kOne, bool kPast>
 __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, int span) {
     __shared__ int pos[MOE_MAX_TOPK];
     __shared__ uint32_t s_max[NT / 64];
@@ -433,12 +433,12 @@ __global__ __launch_bounds__(NT) void sort_move_kernel(SortArgs a, int parts, in
 #pragma unroll
         for (int i = 0; i < NT / 64; ++i) bits = max(bits, s_max[i]);
     }
-    store_pieces<kMode, CH>(a, p, pos, u0, u1, NT, bits);
+    store_pieces<kMode, CH, true, kPast>(a, p, pos, u0, u1, NT, bits);
     if (kMode == kSortCopy && part == 0) copy_scales(a, token, pos, threadIdx.x, NT, scale);
 }
 
 // The counted form's rows of L pieces or fewer, L lanes to a token
-template <SortMode kMode, int L>
+template <SortMode kMode, int L, bool kPast>
 __global__ __launch_bounds__(kThreads) void sort_narrow_kernel(SortArgs a) {
     const int64_t wg = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
     const int64_t mine = wg * (kThreads / L) + threadIdx.x / L, token = min(mine, int64_t(a.T) - 1);
@@ -451,7 +451,7 @@ __global__ __launch_bounds__(kThreads) void sort_narrow_kernel(SortArgs a) {
         bits = lanes_max_u16<L>(pk_max_u16(abs_max8(p[0].v[0]), abs_max8(p[0].v[1])));
     if (mine >= a.T) return;
     const int* const pos = a.inv + token * a.topk;
-    store_pieces<kMode, 1, false>(a, p, pos, u, a.units, L, bits);
+    store_pieces<kMode, 1, false, kPast>(a, p, pos, u, a.units, L, bits);
     if (kMode == kSortCopy) copy_scales(a, token, pos, u, L, scale);
 }
 
@@ -462,7 +462,7 @@ __global__ __launch_bounds__(kThreads) void sort_narrow_kernel(SortArgs a) {
 // ranks its own slots; its first rows are on their way meanwhile.  Two waves to a long
 // row: 1031 x 4096 to int8 12.7 us, one 14.5, four 12.8; 4000 tokens 32.7 / 36.8 / 31.9
 // (11.3 and 30.3 since the ids are on their way before the counters are cleared).
-template <SortMode kMode, int CH, int L>
+template <SortMode kMode, int CH, int L, bool kPast>
 __global__ __launch_bounds__(kBatchThreads) void sort_batch_kernel(SortArgs a, int per, int rep, int span) {
     constexpr int NT = kBatchThreads, kPer = kMaxE / NT, kTeams = NT / L, kWaves = L / 64;
     static_assert(L <= 64 ? CH == 1 : L % 64 == 0, "lanes");
@@ -553,14 +553,14 @@ __global__ __launch_bounds__(kBatchThreads) void sort_batch_kernel(SortArgs a, i
         const int* mine = pos + (t - first) * a.topk;
         for (int u = u0; u < u1; u += L * CH) {
             if (!loaded) load(t, u);
-            store_pieces<kMode, CH, L >= 64>(a, p, mine, u + at_row, u1, L, bits);
+            store_pieces<kMode, CH, L >= 64, kPast>(a, p, mine, u + at_row, u1, L, bits);
             loaded = false;
         }
         if (kMode == kSortCopy && u0 == 0) copy_scales(a, t, mine, at_row, L, scale);
     }
 }
 
-template <SortMode kMode>
+template <SortMode kMode, bool kPast>
 hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
     const int per = batch_tokens(a.T);
     constexpr int kSpan = 1024;                            // pieces of a part
@@ -568,14 +568,14 @@ hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
     int rep = 0;
     while (rep < 3 && (2 * a.E << (rep + 1)) <= 2 * kMaxE) ++rep;
     const int most = std::min(a.units, span);
-    void (*kern)(SortArgs, int, int, int) = most <= 8     ? sort_batch_kernel<kMode, 1, 8>
-                                            : most <= 16  ? sort_batch_kernel<kMode, 1, 16>
-                                            : most <= 32  ? sort_batch_kernel<kMode, 1, 32>
-                                            : most <= 64  ? sort_batch_kernel<kMode, 1, 64>
-                                            : most <= 128 ? sort_batch_kernel<kMode, 1, 128>
-                                            : most <= 256 ? sort_batch_kernel<kMode, 2, 128>
-                                            : most <= 512 ? sort_batch_kernel<kMode, 4, 128>
-                                                          : sort_batch_kernel<kMode, 8, 128>;
+    void (*kern)(SortArgs, int, int, int) = most <= 8     ? sort_batch_kernel<kMode, 1, 8, kPast>
+                                            : most <= 16  ? sort_batch_kernel<kMode, 1, 16, kPast>
+                                            : most <= 32  ? sort_batch_kernel<kMode, 1, 32, kPast>
+                                            : most <= 64  ? sort_batch_kernel<kMode, 1, 64, kPast>
+                                            : most <= 128 ? sort_batch_kernel<kMode, 1, 128, kPast>
+                                            : most <= 256 ? sort_batch_kernel<kMode, 2, 128, kPast>
+                                            : most <= 512 ? sort_batch_kernel<kMode, 4, 128, kPast>
+                                                          : sort_batch_kernel<kMode, 8, 128, kPast>;
     const dim3 grid((a.T + per - 1) / per, (a.units + span - 1) / span);
     return start(kern, grid, kBatchThreads, s, a, per, rep, span);
 }
@@ -587,12 +587,13 @@ hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
 // of 7168 (4.9 M) 13.9 / 12.4.  Few tokens do not fill the batch form's waves.
 bool few_ids(const SortArgs& a, int parts) { return a.T <= 256 || int64_t(a.T) * parts * a.R <= 5 << 19; }
 
-template <SortMode kMode>
+template <SortMode kMode, bool kPast>
 hipError_t launch_narrow(const SortArgs& a, hipStream_t s) {
     const int lanes = a.units <= 8 ? 8 : a.units <= 16 ? 16 : a.units <= 32 ? 32 : 64;
-    void (*kern)(SortArgs) = lanes == 8    ? sort_narrow_kernel<kMode, 8>
-                             : lanes == 16 ? sort_narrow_kernel<kMode, 16>
-                             : lanes == 32 ? sort_narrow_kernel<kMode, 32> : sort_narrow_kernel<kMode, 64>;
+    void (*kern)(SortArgs) = lanes == 8    ? sort_narrow_kernel<kMode, 8, kPast>
+                             : lanes == 16 ? sort_narrow_kernel<kMode, 16, kPast>
+                             : lanes == 32 ? sort_narrow_kernel<kMode, 32, kPast>
+                                           : sort_narrow_kernel<kMode, 64, kPast>;
     return start(kern, grid_of((int64_t(a.T) * lanes + kThreads - 1) / kThreads), kThreads, s, a);
 }
 
@@ -601,11 +602,14 @@ hipError_t launch_move(const SortArgs& a, bool counted, hipStream_t s) {
     // parts of at most NT * CH pieces, of equal length but for the rounding to whole groups
     const int parts = kMode == kSortInt8 ? 1 : (a.units + NT * CH - 1) / (NT * CH);
     const int span = kMode == kSortInt8 ? a.units : ((a.units + parts - 1) / parts + 7) / 8 * 8;
-    if (!counted && !few_ids(a, parts)) return launch_batch<kMode>(a, s);
-    if (counted && a.units <= 64) return launch_narrow<kMode>(a, s);
+    if (!counted && !few_ids(a, parts))
+        return a.past ? launch_batch<kMode, true>(a, s) : launch_batch<kMode, false>(a, s);
+    if (counted && a.units <= 64)
+        return a.past ? launch_narrow<kMode, true>(a, s) : launch_narrow<kMode, false>(a, s);
     const int64_t n = int64_t(a.T) * parts + (counted ? 0 : offset_groups(a.R, a.E));
-    void (*kern)(SortArgs, int, int) =
-        counted ? sort_move_kernel<kMode, NT, CH, false> : sort_move_kernel<kMode, NT, CH, true>;
+    void (*kern)(SortArgs, int, int) = !counted ? sort_move_kernel<kMode, NT, CH, true, false>
+                                       : a.past ? sort_move_kernel<kMode, NT, CH, false, true>
+                                                : sort_move_kernel<kMode, NT, CH, false, false>;
     return start(kern, grid_of(n), NT, s, a, parts, span);
 }
 
@@ -629,7 +633,11 @@ SortPlan plan_sort(int64_t R) {
     return {int(slots), int((R + slots - 1) / slots)};
 }
 
-hipError_t launch_sort_rows(const SortArgs& a, SortMode mode, hipStream_t s) {
+hipError_t launch_sort_rows(const SortArgs& all, SortMode mode, hipStream_t s) {
+    // us as they are / past (8 slots, bf16 rows, and with moe_combine_rows behind): 224 MiB
+    // 39.6 / 51.5 (82 / 97), 448 MiB 106 / 99 (229 / 193), 896 MiB 214 / 187 (432 / 368)
+    SortArgs a = all;
+    a.past = int64_t(a.R) * a.units * 16 >= kLastCacheBytes && whole_lines(a.rows, int64_t(a.units) * 16);
     const SortPlan p = plan_sort(a.R);
     if (p.blocks == 0) return launch_move(a, mode, false, s);
     hipError_t e = start(sort_count_kernel, dim3(p.blocks), kThreads, s, a, p.slots);

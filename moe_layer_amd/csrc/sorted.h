@@ -26,6 +26,7 @@ struct SortArgs {
     int cols;
     int units;                 // 16-byte pieces of a row of `rows`
     int scales;                // scales of a row that is copied or made
+    bool past;                 // rows are stored past the caches' replacement (but in the few-ids form)
 };
 // slots per block of the counted form, and its blocks; 0 blocks where the
 // positions are found without counts
@@ -44,6 +45,7 @@ struct CombineArgs {
     uint16_t* grad_rows;       // bf16 [num_rows, cols]
     float* grad_weights;       // [T, topk] or null
     int T, topk, cols, num_rows;
+    bool past;                 // rows (and grad_rows) go past the caches' replacement
 };
 hipError_t launch_combine_rows(const CombineArgs& a, hipStream_t s);
 hipError_t launch_combine_rows_bwd(const CombineArgs& a, hipStream_t s);
@@ -54,10 +56,48 @@ struct Int8Args {
     float* scales;             // [rows]
     int rows, cols;
     float limit;
+    bool past;                 // x is read past the caches' replacement
 };
 hipError_t launch_quant_int8(const Int8Args& a, bool gated, hipStream_t s);
 
+// The last-level (Infinity) cache.  Rows that are streamed once and are as many bytes
+// go past the replacement of the caches: a stream that cannot stay there reads at up to
+// 6.5 TB/s and is written at up to 6, instead of 5.1, and evicts nothing; smaller ones
+// stay for the kernel that comes next.
+// Written so only where rows are whole lines, and read so where they are that or long:
+// lines that two rows share should meet in a cache (us as they are / past: 8192 tokens
+// of 8 slots, sort 7168 columns 208 / 184, 7176 246 / 249, 5000 166 / 176, 65536 of 1000
+// 277 / 295; combine 204 / 177, 203 / 185, 142 / 130, 226 / 215, 200000 of 328 226 / 234).
+constexpr int64_t kLastCacheBytes = int64_t(256) << 20;
+inline bool whole_lines(const void* rows, int64_t row_bytes) {
+    return (reinterpret_cast<uintptr_t>(rows) | uintptr_t(row_bytes)) % 128 == 0;
+}
+inline bool reads_past(const void* rows, int64_t row_bytes) {
+    return whole_lines(rows, row_bytes) || row_bytes >= 1536;
+}
+
 namespace {
+
+// (kPast is no argument: of two accesses that differ in their caching alone the
+// compiler makes a plain one)
+template <bool kPast>
+__device__ __forceinline__ i32x4 load16(const void* from) {
+    const i32x4* p = static_cast<const i32x4*>(from);
+    if constexpr (kPast) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool kPast>
+__device__ __forceinline__ void store16(void* to, const i32x4& v) {
+    i32x4* p = static_cast<i32x4*>(to);
+    if constexpr (kPast) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
+// f(std::bool_constant<b>())
+template <typename F>
+auto pick(bool b, F f) {
+    return b ? f(std::true_type()) : f(std::false_type());
+}
 
 // ---------------------------------------------------------------------------
 // int8 rows: m = max(|v|max, 1e-10), scale = fl32(m / 127), and the code of v

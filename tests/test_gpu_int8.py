@@ -72,6 +72,20 @@ def test_silu_mul_int8(rows, cols, limit):
     assert same_bits(apart[0], codes) and same_bits(apart[1], scales)
 
 
+@pytest.mark.parametrize("rows,cols,gated", [(33000, 1536, True), (13000, 4096, True), (110000, 464, True),
+                                             (210000, 480, False), (26000, 4096, False), (4000, 32768, False)])
+def test_int8_rows_more_than_the_last_cache_holds(rows, cols, gated):
+    """Inputs of 192 MiB and more: the bits that parts of them give."""
+    d, g = dev(), torch.Generator(device=dev()).manual_seed(rows)
+    x = torch.randn(rows, cols * (2 if gated else 1), generator=g, device=d).bfloat16()
+    assert x.nbytes >= 192 << 20
+    run = (lambda v: ops.moe_silu_mul_int8(v, clamp_limit=2.0)) if gated else ops.moe_quant_act_int8
+    codes, scales = run(x)
+    for lo in range(0, rows, rows // 4):
+        part = run(x[lo: lo + rows // 4])
+        assert same_bits(part[0], codes[lo: lo + rows // 4]) and same_bits(part[1], scales[lo: lo + rows // 4])
+
+
 @pytest.mark.parametrize("cols", [64, 2048, 8192, 32768])
 def test_int8_rows_with_nan_or_infinity(cols):
     """Such a row's scale is NaN, and what a product makes of it; its neighbours

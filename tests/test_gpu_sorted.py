@@ -360,6 +360,67 @@ def test_sort_and_combine_are_each_others_gradients():
 
 # ---------------------------------------------------------- large and apart ---
 
+@pytest.mark.parametrize("T,k,cols,kind,quant", [
+    (4500, 8, 4096, "bf16", None), (9000, 8, 2048, "bf16", None), (9000, 8, 2056, "bf16", None),
+    (300000, 2, 256, "bf16", None), (9000, 8, 4096, "bf16", "int8"), (4600, 8, 8192, "bf16", "fp8"),
+    (9000, 8, 4096, "int8", None)])
+def test_sort_rows_more_than_the_last_cache_holds(T, k, cols, kind, quant):
+    """Rows of 256 MiB and more against torch's stable sort and the quantisers' own rows."""
+    d, E = dev(), 100
+    g = torch.Generator(device=d).manual_seed(T + cols)
+    x, xs = (torch.randn(T, cols, generator=g, device=d).bfloat16(), None) if kind == "bf16" else (
+        torch.randint(-128, 128, (T, cols), generator=g, device=d, dtype=torch.int8), torch.rand(T, generator=g, device=d))
+    ids = torch.randint(-5, E + 5, (T, k), generator=g, device=d, dtype=torch.int32)
+    rows, scales, offsets, inv = ops.moe_sort_rows(x, ids, E, x_scale=xs, quant=quant)
+    assert rows.nbytes >= 256 << 20
+    flat = ids.flatten().long()
+    routed = torch.nonzero((flat >= 0) & (flat < E))[:, 0]
+    order = routed[torch.sort(flat[routed], stable=True).indices]
+    want = torch.full((T * k,), -1, dtype=torch.int32, device=d)
+    want[order] = torch.arange(len(order), dtype=torch.int32, device=d)
+    assert torch.equal(inv.flatten(), want)
+    assert torch.equal(offsets.long(), torch.searchsorted(flat[order].contiguous(), torch.arange(E + 1, device=d)))
+    if quant == "int8":
+        x, xs = ops.moe_quant_act_int8(x)
+    elif quant == "fp8":
+        x, xs = ops.moe_quant_act(x)
+    for lo in range(0, len(order), 8192):
+        part = order[lo: lo + 8192]
+        at = slice(lo, lo + len(part))
+        assert torch.equal(rows[at].view(torch.uint8), x[part // k].view(torch.uint8))
+        assert xs is None or torch.equal(scales[at], xs[part // k])
+
+
+@pytest.mark.parametrize("T,cols", [(4500, 4096), (17000, 1000), (9001, 2056)])
+def test_combine_more_than_the_last_cache_holds(T, cols):
+    """The combine of 256 MiB of rows and more, and its gradient: the bits that parts
+    of the tokens give, which the definition is checked on, and the definition on some."""
+    d, k = dev(), 8
+    g = torch.Generator(device=d).manual_seed(T)
+    rows = torch.randn(T * k, cols, generator=g, device=d).bfloat16()
+    assert rows.nbytes >= 256 << 20
+    inv = torch.randperm(T * k, generator=g, device=d).int().view(T, k)
+    inv[::7, 3] = -1
+    w, grad = torch.rand(T, k, generator=g, device=d), torch.randn(T, cols, generator=g, device=d).bfloat16()
+    out = ops.moe_combine_rows(rows, inv, w)
+    bare = ops.moe_combine_rows(rows, inv)
+    d_rows, d_w = ops.moe_combine_rows_bwd(grad, inv, rows=rows, weights=w)
+    for lo in range(0, T, 2000):
+        part = slice(lo, min(T, lo + 2000))
+        mine = inv[part].flatten()
+        slots = torch.where(mine >= 0, torch.arange(len(mine), device=d, dtype=torch.int32), -1).view(-1, k)
+        few = rows[mine.clamp(min=0).long()]
+        assert torch.equal(ops.moe_combine_rows(few, slots, w[part]), out[part])
+        assert torch.equal(ops.moe_combine_rows(few, slots), bare[part])
+        g_rows, g_w = ops.moe_combine_rows_bwd(grad[part], slots, rows=few, weights=w[part])
+        kept = mine >= 0
+        assert torch.equal(g_rows[kept], d_rows[mine[kept].long()]) and torch.equal(g_w, d_w[part])
+    some = slice(T - 64, T)
+    ref, size = O.combine_rows(bf16_to_f64(rows), inv[some].cpu().numpy(), w[some].cpu().numpy())
+    assert (np.abs(bf16_to_f64(out[some]) - ref) <= (2.0 ** -8 * np.abs(ref) + 2.0 ** -24 * (k + 1) * size)
+            * (1 + 2.0 ** -8)).all()
+
+
 def test_beyond_32_bits():
     """Sources, rows and gradients past 2^32 elements: the last tokens of large
     batches (the first ones are not routed)."""
