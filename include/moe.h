@@ -615,7 +615,7 @@ MOE_API int64_t moe_sort_scratch_bytes(int32_t T, int32_t topk, int32_t E);
  *   inv         device, int32 [T, topk]                             (output)
  *   scratch     device, >= moe_sort_scratch_bytes(T, topk, E) bytes, 4-byte
  *               aligned (may be NULL when that is 0); contents on entry do not
- *               matter; owned by the caller
+ *               matter; not for two calls that may run at the same time
  * No output (and no scratch) may overlap an input or another output.  T == 0
  * sets the offsets to 0.  Requires 1 <= E <= MOE_MAX_EXPERTS, 1 <= topk <=
  * MOE_MAX_TOPK, T * topk <= 2^30, cols % 8 == 0 for bf16, % 128 for FP8_E4M3,

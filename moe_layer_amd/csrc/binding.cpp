@@ -372,6 +372,9 @@ PyObject* py_sort_rows(PyObject*, PyObject* const* v, Py_ssize_t n) {
             x.is({E4M3, U8}, {T, cols});
             xs.is({F32}, {T, cols / 128});
         }
+        const int32_t t = size32(T, "x"), c = size32(cols, "x"), k = size32(topk, "topk_ids");
+        const int64_t bytes = g_sort_bytes(t, k, int32_t(E));   // (and its checks, before anything is allocated)
+        if (bytes < 0) return PyLong_FromLong(long(bytes));
         const int64_t R = T * topk;
         // fp8 rows made from bf16 ones are uint8 as moe_quant_act's are, copied ones of x's own type
         const auto as = type == kBf16 ? BF16 : type == kInt8 ? I8 : bf16 ? U8 : x.t->scalar_type();
@@ -386,9 +389,6 @@ PyObject* py_sort_rows(PyObject*, PyObject* const* v, Py_ssize_t n) {
             need(scratch.t->is_contiguous(), "scratch", "must be contiguous");
         }
         on_gpu(*x.t, {&ids, &xs, &rows.arg, &scales.arg, &offsets.arg, &inv.arg, &scratch});
-        const int32_t t = size32(T, "x"), c = size32(cols, "x"), k = size32(topk, "topk_ids");
-        const int64_t bytes = g_sort_bytes(t, k, int32_t(E));
-        if (bytes < 0) return PyLong_FromLong(long(bytes));
         at::Tensor own;
         if (!scratch.t && bytes > 0) own = at::empty({bytes}, x.t->options().dtype(U8));
         void* ws = own.defined() ? own.data_ptr() : scratch.ptr();
