@@ -46,9 +46,9 @@ constexpr Tile kTilesBf16[] = {
 };
 // int8: from the bf16 constants (as many bytes that go to the matrix cores as they
 // are) by a search for the ones whose picks are the fastest over 347 shapes, dense
-// and grouped, each timed in every tile: 2.4 % slower than the best tile in the
-// geometric mean, 37 % at worst (1742 rows in 8 groups of 624 x 3440); fitted to half
-// of them 2.8 % over the other half.  Without the two workgroups a CU of the last one
+// and grouped, each timed in every tile: 2.3 % slower than the best tile in the
+// geometric mean, 45 % at worst (1568 rows in 100 groups of 360 x 128, 6.5 us); fitted
+// to half of them 2.8 % over the other half.  Without the two workgroups a CU of the last one
 // the best tile were 48 % slower at worst (7189 rows in 256 groups of 504 x 256).
 constexpr Tile kTilesInt8[] = {
     {true, 0, 16, 16, 1.18f, 1.14f, 0.0561f},    {true, 1, 32, 16, 1.20f, 1.52f, 0.0748f},

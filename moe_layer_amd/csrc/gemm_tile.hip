@@ -345,11 +345,11 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
 // turn, so the next stage's tokens and the weights of the one after are on their way
 // while a stage is read: unit n goes where unit n - 5 was.
 //
-// 8192 x 4096 x 7168, operands random over all codes: 178 us, 2.70 POP/s (a library
+// 8192 x 4096 x 7168, operands random over all codes: 180-186 us, 2.6 POP/s (a library
 // product 195 us; this tile with all waves in step 204).  What bounds it is power: the
 // same product of zeros takes 137 us, 3.52 POP/s, at the rate of the matrix
 // instructions alone.  Four waves of 128 x 128 outputs, which read a third less from
-// LDS, took 182, and longer for short K.
+// LDS, took 182 against 178 in the same run, and longer for short K.
 template <bool NTW>
 __device__ __forceinline__ void tile_product_int8(const RowsGemmArgs& g, lds_t* lds, int e, int row0, int row1,
                                                   int n0) {
