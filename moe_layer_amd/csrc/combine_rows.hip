@@ -6,7 +6,7 @@
 // its weight's gradient is 0.
 //
 // Every row is read once and every output written once, so both are bound by bytes:
-// the combine of 8192 x 7168 and 8 slots 179 us, 5.9 TB/s (a large copy 5.1); the
+// the combine of 8192 x 7168 and 8 slots 179-193 us, 5.5-5.9 TB/s (a large copy 5.1); the
 // gradient of 4096 x 4096 and 8 slots 113 us, 5.05 TB/s.  A thread has one piece of 16
 // bytes of a token, which fills the CUs from a few tokens on, with the loads of eight
 // slots in flight; gathering by token needs no atomics and sums in slot order.
@@ -188,7 +188,8 @@ hipError_t launch_bwd(const CombineArgs& a, hipStream_t s) {
 }
 
 // Whether there are more rows than stay in the last-level cache (us as they are / past
-// it: the combine of 224 MiB 39.4 / 46.5, 448 MiB 104 / 93, 896 MiB 206 / 178; its
+// it: the combine of 224 MiB 39.4 / 46.5, 448 MiB 104 / 93, 896 MiB 206 / 178 (an
+// output whose last lines are in the cache yet; 206 / 193 otherwise); its
 // gradient, rows read and written, of 224 MiB 105 / 102, 256 MiB 118 / 113, 896 MiB 405 /
 // 395.  The combine's output is left to the caches: 179 / 183)
 bool streamed(const CombineArgs& a) {

@@ -13,8 +13,8 @@
 //               (sort_place_kernel), then the rows are moved: three launches, for
 //               more ids than every workgroup should read.
 // A row is read once and stored topk times: large batches are bound by those bytes
-// (8192 x 7168 bf16 to 8 of 128 experts 187 us, 5.7 TB/s, 10 of them to find the
-// positions), single tokens by the launch (kernel 2.8 us), batches in between by the
+// (8192 x 7168 bf16 to 8 of 128 experts 187 us, x from the last-level cache, 216 with x
+// from HBM, 4.9 TB/s; 10 of them to find the positions), single tokens by the launch (kernel 2.8 us), batches in between by the
 // look at all ids in front (1031 x 4096 to int8 11.3 us, 8.3 of them bytes).
 #include "dev_align.h"
 #include "moe.h"
@@ -635,7 +635,9 @@ SortPlan plan_sort(int64_t R) {
 
 hipError_t launch_sort_rows(const SortArgs& all, SortMode mode, hipStream_t s) {
     // us as they are / past (8 slots, bf16 rows, and with moe_combine_rows behind): 224 MiB
-    // 39.6 / 51.5 (82 / 97), 448 MiB 106 / 99 (229 / 193), 896 MiB 214 / 187 (432 / 368)
+    // 39.6 / 51.5 (82 / 97), 448 MiB 106 / 99 (229 / 193), 896 MiB 213 / 187 (432 / 368): x,
+    // an eighth of it, stays in the cache for all its reads.  Where x is not there to begin
+    // with, 213 / 216.
     SortArgs a = all;
     a.past = int64_t(a.R) * a.units * 16 >= kLastCacheBytes && whole_lines(a.rows, int64_t(a.units) * 16);
     const SortPlan p = plan_sort(a.R);
