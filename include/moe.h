@@ -606,8 +606,9 @@ MOE_API int64_t moe_sort_scratch_bytes(int32_t T, int32_t topk, int32_t E);
  *   x_scale     device, fp32 [T, cols / 128] (FP8_E4M3), [T] (INT8), else NULL
  *   topk_ids    device, int32 [T, topk]
  *   rowtype     xtype, or, where xtype is MOE_WDTYPE_BF16, MOE_WDTYPE_FP8_E4M3
- *               or MOE_WDTYPE_INT8: x is quantised on the way by moe_quant_act's
- *               or moe_quant_act_int8's rule
+ *               or MOE_WDTYPE_INT8: x is quantised on the way, to the codes and
+ *               scales that moe_quant_act (of x with NaN and infinities too; a
+ *               signaling NaN as of a quiet one) or moe_quant_act_int8 gives
  *   rows        device, [T * topk, cols] of rowtype                 (output)
  *   row_scales  device, fp32 [T * topk, cols / 128] or [T * topk]; NULL for bf16
  *               rows, 4-byte aligned                                (output)

@@ -147,20 +147,35 @@ __device__ __forceinline__ uint2 int8_codes(const i32x4& w, float inverse) {
     return uint2{pair[0] | pair[1] << 16, pair[2] | pair[3] << 16};
 }
 
-// fp8 codes (moe_quant_act's rule) of 16 columns by each of 8 neighbouring lanes,
-// which hold a 128-column group; returns the scale
+// fp8 codes and scale, moe_quant_act's bit for bit, of 16 columns by each of 8
+// neighbouring lanes, which hold a 128-column group; returns the scale.  Its maximum
+// passes over a NaN, whose code is -448's, and an infinity makes the scale infinite and
+// its inverse 0.
 __device__ __forceinline__ float quant16(const i32x4& a, const i32x4& b, i32x4& codes) {
     uint32_t m = pk_max_u16(abs_max8(a), abs_max8(b));
     m = dpp_max_u16<0xb1>(m);                              // quad_perm [1,0,3,2]
     m = dpp_max_u16<0x4e>(m);                              // quad_perm [2,3,0,1]
     m = dpp_max_u16<0x141>(m);                             // row_half_mirror
-    const float s = fp8_group_scale(__uint_as_float(max(m & 0xffffu, m >> 16) << 16));
-    const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));   // 1 / s, as in quant8
+    m = max(m & 0xffffu, m >> 16);
+    if (m > 0x7f80u) {                                     // a NaN, above every number's bits (the 8 lanes alike)
+        auto number = [](uint32_t h) { return h > 0x7f80u ? 0u : h; };
+        m = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            m = max(max(m, number(uint32_t(a[q]) & 0x7fffu)), number(uint32_t(a[q]) >> 16 & 0x7fffu));
+            m = max(max(m, number(uint32_t(b[q]) & 0x7fffu)), number(uint32_t(b[q]) >> 16 & 0x7fffu));
+        }
+        m = dpp_max_u16<0x141>(dpp_max_u16<0x4e>(dpp_max_u16<0xb1>(m)));
+    }
+    const float s = fp8_group_scale(__uint_as_float(m << 16));
+    // 1 / s, as in quant8; an infinity's mirrored exponent is below 0
+    const float inv = __int_as_float(max(int(254u << 23) - __float_as_int(s), 0));
+    // the clamp is for what no number is: the middle of three takes a NaN for the lowest
+    auto code = [&](float v) { return __builtin_amdgcn_fmed3f(__fmul_rn(v, inv), -448.0f, 448.0f); };
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const uint32_t w0 = uint32_t(q < 2 ? a[2 * q] : b[2 * q - 4]), w1 = uint32_t(q < 2 ? a[2 * q + 1] : b[2 * q - 3]);
-        codes[q] = int(pack_e4m3(__fmul_rn(bf16_lo(w0), inv), __fmul_rn(bf16_hi(w0), inv), __fmul_rn(bf16_lo(w1), inv),
-                                 __fmul_rn(bf16_hi(w1), inv)));
+        codes[q] = int(pack_e4m3(code(bf16_lo(w0)), code(bf16_hi(w0)), code(bf16_lo(w1)), code(bf16_hi(w1))));
     }
     return s;
 }
