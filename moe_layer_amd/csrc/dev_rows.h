@@ -192,19 +192,14 @@ __device__ __forceinline__ void stage4(lds_t* tile, int t, int n, const f32x4& v
 
 // Eight outputs per lane by THREADS neighbouring lanes, 16 bytes a store wherever a
 // row starts (global stores take any alignment; 6565 x 5413 x 496 int8 54.7 -> 45.2 us
-// against 2 bytes a store where N is odd), the last N % 8 of a row one by one.  NT:
-// past the caches' replacement (tile_product), but for long outputs whose rows are no
-// whole lines: the two halves of a line that tiles share should meet in L2 (us past it
-// / not: 8140 x 3448 x 1152, 56 MB, 44.2 / 38.3, 6565 x 5413 x 496, 71 MB, 52.1 /
-// 44.1; 5009 x 1642 x 592, 16 MB, 15.3 / 16.8, 3937 rows in 100 groups of 3368 x 384,
-// 27 MB, 34.4 / 36.4).
-template <int BW, int BT, int THREADS, bool NT>
-__device__ __forceinline__ void store_tile(const RowsGemmArgs& g, const lds_t* tile, int row0, int row1, int n0) {
+// against 2 bytes a store where N is odd), the last N % 8 of a row one by one.  kPast:
+// past the caches' replacement, of rows that are whole lines.
+template <int BW, int BT, int THREADS, bool kPast>
+__device__ __forceinline__ void store_rows(const RowsGemmArgs& g, const lds_t* tile, int row0, int row1, int n0) {
     typedef __attribute__((ext_vector_type(4), aligned(2))) int anywhere_v4;
     typedef const __attribute__((address_space(3))) uint16_t lds_u16;
     constexpr int kPer = BW / 8, kTurns = (BT * kPer + THREADS - 1) / THREADS;
     const int live = min(BT, row1 - row0);
-    const bool past = NT && ((g.N & 63) == 0 || int64_t(g.rows) * g.N < 16 << 20);
     // several pieces read ahead of their stores
 #pragma unroll(kTurns < 8 ? kTurns : 4)
     for (int q = 0; q < kTurns; ++q) {
@@ -213,14 +208,34 @@ __device__ __forceinline__ void store_tile(const RowsGemmArgs& g, const lds_t* t
         if (r >= live || n0 + c >= g.N) continue;
         const lds_t* const from = tile + r * kOutRow<BW> + 2 * c;
         uint16_t* const to = g.out + int64_t(row0 + r) * g.N + n0 + c;
-        if (n0 + c + 8 <= g.N) {
-            const i32x4 v = *reinterpret_cast<lds_v4*>(from);
-            if (past) __builtin_nontemporal_store(v, reinterpret_cast<anywhere_v4*>(to));
-            else *reinterpret_cast<anywhere_v4*>(to) = v;
+        if constexpr (kPast) {
+            __builtin_nontemporal_store(*reinterpret_cast<lds_v4*>(from), reinterpret_cast<i32x4*>(to));
+        } else if (n0 + c + 8 <= g.N) {
+            *reinterpret_cast<anywhere_v4*>(to) = *reinterpret_cast<lds_v4*>(from);
         } else {
             for (int k = 0; n0 + c + k < g.N; ++k) to[k] = *reinterpret_cast<lds_u16*>(from + 2 * k);
         }
     }
+}
+// NT: tiles of 256 weight rows.  Outputs whose rows are whole lines go past the caches'
+// replacement; of others the two halves of a line that tiles share should meet in L2.
+// The choice stands around the loops: of two stores in one the compiler makes a plain
+// one.  us past it / not, and with moe_silu_mul reading the result; whole lines:
+// bf16 3000 x 2048 x 512 12.0 / 12.9 (20.3 / 21.1), 8000 rows in 32 groups of 5120 x 640
+// 70 / 81 (103 / 102), 8192 x 8192 x 1024 123 / 121 (152 / 150); fp8 6000 in 16 of 1024 x
+// 1024 19.1 / 20.4 (25.1 / 25.8), 8192 x 8192 x 1024 136 / 138 (169 / 168); int8 the two
+// 12.9 / 14.3 (18.7 / 20.0), 77.8 / 78.3 (108 / 108), 32768 in 128 of 4096 x 1536 288 /
+// 293 (344 / 350).  Not: bf16 16384 x 2064 x 512 59 / 54 (74 / 70), 8192 x 8192 x 1024
+// 16 bytes off a line 134 / 123 (160 / 152), 8000 in 32 of 5136 x 640 77 / 83 (106 / 104);
+// fp8 16384 x 2064 x 512 60 / 54 (77 / 71); int8 35.7 / 33.5 (52 / 50), 8192 x 8192 x 1024
+// off a line 89 / 79 (115 / 109), 4000 x 2080 x 2048 24.6 / 26.2 (30.8 / 32.2).
+template <int BW, int BT, int THREADS, bool NT>
+__device__ __forceinline__ void store_tile(const RowsGemmArgs& g, const lds_t* tile, int row0, int row1, int n0) {
+    if constexpr (NT) {
+        if (((reinterpret_cast<uintptr_t>(g.out) | 2 * uintptr_t(g.N)) & 127) == 0)
+            return store_rows<BW, BT, THREADS, true>(g, tile, row0, row1, n0);
+    }
+    store_rows<BW, BT, THREADS, false>(g, tile, row0, row1, n0);
 }
 
 // One operand of a 16-row subtile for a 128-byte step of K, from this lane's two

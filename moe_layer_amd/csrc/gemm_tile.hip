@@ -299,9 +299,7 @@ __device__ __forceinline__ void tile_product(const RowsGemmArgs& g, lds_t* ring,
     }
     // The ring is idle: each wave's outputs pass through 16 rows of its own, as
     // it needs no other wave.  The stores of 256 weight rows, long streams for
-    // the most part, are past the caches' replacement: 32768 x 4096 x 1536 in 128
-    // bf16 groups 574 -> 550 us, and 635 -> 623 us with moe_silu_mul reading the
-    // result.
+    // the most part, may go past the caches' replacement (store_tile).
     __syncthreads();
     constexpr int kCols = BW / WW;
     lds_t* const rows16 = ring + wv * (16 * kOutRow<kCols>);
