@@ -113,18 +113,21 @@ __device__ __forceinline__ int count_blocks(const RowsGemmArgs& g) {
 // count_blocks and find_block for the same BM with one look at the offsets: up to
 // kHeldGroups groups stay in the wave's registers, four a lane.  Every workgroup starts
 // with this and loads nothing before (188 rows in 256 int8 groups of 440 x 368 10.2 ->
-// 7.0 us, 131 in 128 of 4096 x 1536 76 -> 70, 32768 in 128 300 -> 292).
-template <int BM>
+// 7.0 us, 131 in 128 of 4096 x 1536 76 -> 70, 32768 in 128 300 -> 292).  Of more groups
+// the offsets are read for each; kTotal false: only to find a block (1 row in 1024 fp8
+// groups of 496 x 1280 7.9 us, with the count in front 10.1; 10 in 512 bf16 ones of 352 x
+// 1792 6.8, 8.1).
+template <int BM, bool kTotal>
 struct RowBlocks {
     static constexpr int kPer = 4, kHeldGroups = 64 * kPer;
     int lo[kPer], hi[kPer];
     int own, sum;            // the lane's blocks, and with those of the lanes before
-    int total;
+    int total;               // (kTotal)
     bool held;
 
     __device__ __forceinline__ explicit RowBlocks(const RowsGemmArgs& g) : held(g.offsets && g.E <= kHeldGroups) {
         if (!held) {
-            total = count_blocks<BM>(g);
+            if constexpr (kTotal) total = count_blocks<BM>(g);
             return;
         }
         const int lane = threadIdx.x & 63;

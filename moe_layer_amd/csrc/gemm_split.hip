@@ -45,7 +45,7 @@ __global__ __launch_bounds__(64 * W) void rows_split_kernel(RowsGemmArgs g, int 
     const int slot = gridDim.y == 1 ? int(blockIdx.x / uint32_t(ntiles)) : int(item / ntiles);
     const int tile = int(item - int64_t(slot) * ntiles);
     int e, row0, row1;
-    if (slot >= slots || !RowBlocks<BT>(g).find(g, slot, e, row0, row1)) return;   // the whole workgroup alike
+    if (slot >= slots || !RowBlocks<BT, false>(g).find(g, slot, e, row0, row1)) return;   // the whole workgroup alike
 
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

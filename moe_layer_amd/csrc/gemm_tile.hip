@@ -633,7 +633,7 @@ __device__ __forceinline__ void tile_product_pair(const RowsGemmArgs& g, lds_t* 
 template <int BW, int BT>
 __device__ __forceinline__ bool find_tile(const RowsGemmArgs& g, int ntiles, int band, int& e, int& row0, int& row1,
                                           int& n0) {
-    const RowBlocks<BT> blocks(g);
+    const RowBlocks<BT, true> blocks(g);
     const int64_t total = int64_t(blocks.total) * ntiles;
     int64_t item;
     if (!xcd_item(total, item)) return false;                // the whole workgroup alike
