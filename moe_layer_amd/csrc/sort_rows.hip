@@ -32,9 +32,8 @@ constexpr int kThreads = 256, kPlaceThreads = 1024;
 constexpr int kBatchMostSlots = 49152;
 constexpr int kMostBlocks = 256;
 constexpr int kBatchThreads = 512;
-// tokens of a workgroup of the batch form: about 512 workgroups
-constexpr int batch_tokens(int T) { return (T + 2047) / 2048 * 4; }
-// and its slots, at most kBatchMostSlots / 512 of T / 512 tokens and those of 4 more
+constexpr int kBatchSpan = 1024;                           // pieces of a part of a row that is not int8's
+// slots of a workgroup of the batch form, at most kBatchMostSlots / 512 of T / 512 tokens and those of 4 more
 constexpr int kBatchSlots = kBatchMostSlots / 512 + 4 * MOE_MAX_TOPK;
 
 template <int CTRL>
@@ -118,12 +117,6 @@ __device__ __forceinline__ void each_id(const int32_t* p, int n, F f) {
     ids.each(f);
 }
 
-// Ids up to which a wave holds them all, for the positions of a token's slots, and
-// workgroups of 16 experts each compare them, for the offsets; more are counted in LDS
-// (us in a graph, 8 of 256 experts, to int8, held / counted: 16 x 4096 3.6 / 4.9, 64 x
-// 4096 3.9 / 5.2, 128 x 4096 4.4 / 4.9).
-constexpr int kHeldIds = 1024;
-
 // Workgroups that write the offsets beside those that move rows
 constexpr int offset_groups(int R, int E) { return R <= kHeldIds ? E / 16 + 1 : 1; }
 
@@ -199,7 +192,7 @@ __device__ __forceinline__ void compare_held(const SortArgs& a, int t, int* pos)
 // many ids eight slots at a time, every wave counting over its share of the ids
 template <int NT>
 __device__ __forceinline__ void find_positions(const SortArgs& a, int t, int* pos) {
-    constexpr int kAt = 8;
+    constexpr int kAt = kSlotsAtOnce;
     const int lane = threadIdx.x & 63, own = t * a.topk;
     if (a.R <= 64) return compare_held<NT, 1>(a, t, pos);
     if (a.R <= 256) return compare_held<NT, 4>(a, t, pos);
@@ -563,8 +556,7 @@ __global__ __launch_bounds__(kBatchThreads) void sort_batch_kernel(SortArgs a, i
 template <SortMode kMode, bool kPast>
 hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
     const int per = batch_tokens(a.T);
-    constexpr int kSpan = 1024;                            // pieces of a part
-    const int span = kMode == kSortInt8 ? a.units : kSpan;
+    const int span = kMode == kSortInt8 ? a.units : kBatchSpan;
     int rep = 0;
     while (rep < 3 && (2 * a.E << (rep + 1)) <= 2 * kMaxE) ++rep;
     const int most = std::min(a.units, span);
@@ -579,13 +571,6 @@ hipError_t launch_batch(const SortArgs& a, hipStream_t s) {
     const dim3 grid((a.T + per - 1) / per, (a.units + span - 1) / span);
     return start(kern, grid, kBatchThreads, s, a, per, rep, span);
 }
-
-// Whether few ids are read so few times that every workgroup may compare them all
-// (sort_move_kernel<.., true>): ids read in all, us in that form / in the batch
-// form: 8 experts, 512 tokens of 4096 to int8 (2.0 M) 8.2 / 8.5, 300 of 7168 in four
-// parts (2.8 M) 10.8 / 11.2; 600 to int8 (2.8 M) 10.8 / 8.9, 700 (3.7 M) 11.8 / 9.2, 400
-// of 7168 (4.9 M) 13.9 / 12.4.  Few tokens do not fill the batch form's waves.
-bool few_ids(const SortArgs& a, int parts) { return a.T <= 256 || int64_t(a.T) * parts * a.R <= 5 << 19; }
 
 template <SortMode kMode, bool kPast>
 hipError_t launch_narrow(const SortArgs& a, hipStream_t s) {
@@ -602,7 +587,8 @@ hipError_t launch_move(const SortArgs& a, bool counted, hipStream_t s) {
     // parts of at most NT * CH pieces, of equal length but for the rounding to whole groups
     const int parts = kMode == kSortInt8 ? 1 : (a.units + NT * CH - 1) / (NT * CH);
     const int span = kMode == kSortInt8 ? a.units : ((a.units + parts - 1) / parts + 7) / 8 * 8;
-    if (!counted && !few_ids(a, parts))
+    const int batch_parts = kMode == kSortInt8 ? 1 : (a.units + kBatchSpan - 1) / kBatchSpan;
+    if (!counted && !few_ids(a.T, a.topk, parts, batch_parts, a.units))
         return a.past ? launch_batch<kMode, true>(a, s) : launch_batch<kMode, false>(a, s);
     if (counted && a.units <= 64)
         return a.past ? launch_narrow<kMode, true>(a, s) : launch_narrow<kMode, false>(a, s);

@@ -34,6 +34,39 @@ struct SortPlan {
     int slots, blocks;
 };
 SortPlan plan_sort(int64_t R);
+
+// Ids up to which a wave holds them all, for the positions of a token's slots, and
+// workgroups of 16 experts each compare them, for the offsets; more are counted in LDS
+// (us in a graph, 8 of 256 experts, to int8, held / counted: 16 x 4096 3.6 / 4.9, 64 x
+// 4096 3.9 / 5.2, 128 x 4096 4.4 / 4.9).
+constexpr int kHeldIds = 1024;
+// slots of a token whose positions are found with one look at all of more ids
+constexpr int kSlotsAtOnce = 8;
+// tokens of a workgroup of the batch form: about 512 workgroups
+constexpr int batch_tokens(int T) { return std::max((T + 2047) / 2048, 1) * 4; }
+
+// Whether the workgroups that move `parts` parts of every token's row of `units` pieces
+// compare its slots with all ids themselves, or, in the batch form, `batch_parts` parts
+// to a workgroup's tokens, count the ids for several tokens at once.  Comparing reads
+// all ids again for every kSlotsAtOnce slots.  That many reads in all are made in the
+// time of the batch form's start where it has workgroups enough; fewer than 96 of them
+// take longer, for their tokens have all slots' rows to store.  And one workgroup's
+// reads, one after the other, take the time of its row.
+// us, comparing / batch, with the reads in all, of 256 experts: 8 slots: 256 x 7168 (2.1 M)
+// 9.7 / 11.3, 320 x 7168 (3.3) 11.9 / 12.2, 400 (5.1) 15.0 / 13.3, 512 x 4096 to int8 (2.1)
+// 9.0 / 9.1, 700 (3.9) 12.7 / 10.0; 16 slots: 128 x 7168 (2.1) 10.9 / 14.4, 256 x 7168 (8.4)
+// 19.0 / 15.8; 64 slots: 32 x 7168 (2.1) 23.7 / 35.1, 32 x 2048 (0.5) 22.2 / 15.2, 64 x 16384
+// (17) 44 / 41, 256 x 2048 (34) 81 / 20, 256 x 7168 (134) 153 / 42.  Over 1082 shapes from
+// 1 to 1000 tokens of 512 to 65536 columns 0.7 % slower than the faster form in the
+// geometric mean, 32 % at worst.
+constexpr bool few_ids(int T, int topk, int parts, int batch_parts, int units) {
+    const int64_t R = int64_t(T) * topk;
+    const int64_t reads = R * (R > kHeldIds ? (topk + kSlotsAtOnce - 1) / kSlotsAtOnce : 1);
+    const int64_t batch = int64_t((T + batch_tokens(T) - 1) / batch_tokens(T)) * batch_parts;
+    return reads <= 6144 * int64_t((units + 255) / 256) &&
+           T * reads * parts * std::min<int64_t>(batch, 96) <= (int64_t(5) << 19) * 96;
+}
+
 hipError_t launch_sort_rows(const SortArgs& a, SortMode mode, hipStream_t s);
 
 struct CombineArgs {
