@@ -62,3 +62,138 @@ def test_sort_to_fp8_is_moe_quant_act_whatever_the_values(T, k, cols):
         at = inv[:, j].long()
         assert torch.equal(rows[at], codes)
         assert torch.equal(row_scales[at].view(torch.int32), scales.view(torch.int32))
+
+
+# ------------------------------------------------- the form with scratch ---
+
+COUNTED = dict(T=13001, k=4, E=100, cols=128)             # 52004 slots: counted, placed and moved
+
+
+def counted_case(seed, T, k, E, cols):
+    rng, g = np.random.default_rng(seed), torch.Generator().manual_seed(seed)
+    ids = rng.integers(-3, E + 3, (T, k)).astype(np.int32)
+    x = torch.randn(T, cols, generator=g).bfloat16()
+    return torch.from_numpy(ids), x, O.sort_slots(ids, E)
+
+
+def check_counted(x, want, rows, offsets, inv):
+    want_off, want_inv, token = want
+    np.testing.assert_array_equal(offsets.cpu().numpy(), want_off)
+    np.testing.assert_array_equal(inv.cpu().numpy(), want_inv)
+    n = int(want_off[-1])
+    np.testing.assert_array_equal(rows[:n].view(torch.int16).cpu().numpy(), x.view(torch.int16).numpy()[token])
+    assert (rows[n:] == 7).all(), "rows behind the last one were written"
+
+
+class Buffers:
+    """A caller's operands and outputs, and scratch of the size asked for with a guard behind it."""
+
+    def __init__(self, T, k, E, cols):
+        d, n = dev(), ops.moe_sort_scratch_bytes(T, k, E)
+        assert n > 0
+        self.x, self.ids = torch.zeros(T, cols, dtype=torch.bfloat16, device=d), torch.zeros(T, k, dtype=torch.int32, device=d)
+        self.rows = torch.empty(T * k, cols, dtype=torch.bfloat16, device=d)
+        self.offsets, self.inv = torch.empty(E + 1, dtype=torch.int32, device=d), torch.empty(T, k, dtype=torch.int32, device=d)
+        self.room = torch.empty(n + 256, dtype=torch.uint8, device=d)
+        self.scratch, self.E = self.room[:n], E
+
+    def fill(self, x, ids):
+        self.x.copy_(x)
+        self.ids.copy_(ids)
+        self.rows.fill_(7)
+        self.scratch.fill_(0xff)
+        self.room[self.scratch.numel():] = 0xa5
+
+    def sort(self):
+        return ops.moe_sort_rows(self.x, self.ids, self.E, rows=self.rows, offsets=self.offsets, inv=self.inv,
+                                 scratch=self.scratch)
+
+    def check(self, x, want):
+        check_counted(x, want, self.rows, self.offsets, self.inv)
+        assert (self.room[self.scratch.numel():] == 0xa5).all(), "wrote behind the scratch"
+
+
+def test_counted_sort_in_a_callers_scratch():
+    """Exactly the bytes asked for, whatever they hold; one byte less is refused."""
+    b = Buffers(**COUNTED)
+    for seed in (1, 2):
+        ids, x, want = counted_case(seed, **COUNTED)
+        b.fill(x, ids)
+        b.sort()
+        b.check(x, want)
+    b.scratch = b.scratch[:-1]
+    with pytest.raises(ops.MoeError):
+        b.sort()
+
+
+def test_counted_sort_replays():
+    """Its three launches from a captured graph: every replay, on other rows and ids
+    and with eager work and synchronisation between them, against the definition."""
+    b = Buffers(**COUNTED)
+    ids, x, want = counted_case(0, **COUNTED)
+    b.fill(x, ids)
+    b.sort()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.sort()
+    other = Buffers(**COUNTED)
+    for seed in range(3, 8):
+        ids, x, want = counted_case(seed, **COUNTED)
+        b.fill(x, ids)
+        graph.replay()
+        if seed % 2:
+            torch.cuda.synchronize()
+        other.fill(x, ids)
+        other.sort()
+        b.check(x, want)
+        other.check(x, want)
+
+
+def test_counted_sort_on_two_streams_of_two_threads():
+    """Two threads, a stream, rows and a scratch each, sorting at once."""
+    import threading
+
+    sets = [(Buffers(**COUNTED), [counted_case(10 * i + j, **COUNTED) for j in range(4)]) for i in range(2)]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(b, cases):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for ids, x, want in cases:
+                    b.fill(x, ids)
+                    for _ in range(3):
+                        b.sort()
+                    b.check(x, want)
+        except BaseException as e:   # noqa: BLE001 (told to the test's own thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=s) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+# -------------------------------------------------- launches cut in two ---
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_combine_of_more_columns_than_a_launch_takes(weighted):
+    """T * cols / 8 past 2^31 - 1: the tokens behind that are a launch of their own,
+    with their own slots, weights and outputs.  Weights are powers of two and a token
+    has one slot, so outputs are exact."""
+    d, cols, n = dev(), 8192, 40
+    T = (2 ** 31 - 1) // (cols // 8) + 700
+    g = torch.Generator(device=d).manual_seed(3)
+    rows = torch.randn(n, cols, generator=g, device=d).bfloat16()
+    inv = torch.randint(-1, n, (T, 1), generator=g, device=d, dtype=torch.int32)
+    w = torch.exp2(torch.randint(-3, 4, (T, 1), generator=g, device=d).float()) if weighted else None
+    out = ops.moe_combine_rows(rows, inv, w)
+    for lo in range(0, T, 1 << 17):
+        part = slice(lo, min(T, lo + (1 << 17)))
+        want = torch.where(inv[part] >= 0, rows[inv[part, 0].clamp(min=0).long()].float(), 0.0)
+        if weighted:
+            want *= w[part]
+        assert torch.equal(out[part], want.bfloat16()), lo
