@@ -377,9 +377,7 @@ __device__ __forceinline__ void tile_product_int8(const RowsGemmArgs& g, lds_t* 
         const int step = st + turn < steps ? st + turn : st + turn - steps;
         const uint8_t* from = (weights ? wbase : abase) + (int64_t(step) << 7) + (weights ? woff[j] : aoff[j]);
         if (step == part && past) from = kNoChunk;
-        lds_t* const to = lds + unit * kUnit + (wv + 8 * j) * 1024;
-        if (NTW && weights) load_piece<true>(from, to, true);
-        else load_piece<false>(from, to, weights);
+        load_piece<NTW>(from, lds + unit * kUnit + (wv + 8 * j) * 1024, weights);
     };
     auto issue = [&](bool weights, int st, int unit) {
 #pragma unroll

@@ -23,7 +23,6 @@ struct SortArgs {
     int32_t* inv;              // [T, topk]
     int32_t* counts;           // scratch [blocks, E]
     int T, topk, E, R;         // R = T * topk
-    int cols;
     int units;                 // 16-byte pieces of a row of `rows`
     int scales;                // scales of a row that is copied or made
     bool past;                 // rows are stored past the caches' replacement (but in the few-ids form)

@@ -110,7 +110,6 @@ MOE_API int moe_sort_rows(const void* x, const float* x_scale, const int32_t* to
     a.topk = topk;
     a.E = E;
     a.R = int(R);
-    a.cols = cols;
     a.units = int(rb / 16);
     a.scales = rs;
     const SortMode mode = xtype == rowtype ? kSortCopy : to_int8 ? kSortInt8 : kSortFp8;
