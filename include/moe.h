@@ -652,7 +652,9 @@ MOE_API int moe_combine_rows(const void* rows, const int32_t* inv, const float* 
  * Slots whose inv lies outside [0, num_rows) have no row and grad_weights 0.
  * Rows that no slot has are not written.  A row has one slot, as moe_sort_rows
  * makes them: of one that several name, each value of grad_rows is one of theirs,
- * unspecified which, and not their sum.
+ * unspecified which, and not their sum.  Nothing calls this but its user: the
+ * binding records none of these operators for torch's autograd, and the products
+ * in between have no gradient here.
  *
  *   grad_out      device, bf16 [T, cols]
  *   rows          device, bf16 [num_rows, cols]; NULL where grad_weights is NULL

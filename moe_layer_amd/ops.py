@@ -568,7 +568,9 @@ def moe_sort_rows(x: torch.Tensor, topk_ids: torch.Tensor, E: int, x_scale=None,
     Returns (rows [T * topk, cols], scales, offsets int32 [E+1], inv int32 [T,
     topk]): slot (t, j) is row inv[t, j], -1 when its id is outside [0, E);
     scales is None for bf16 rows.  Rows from offsets[E] on keep what they held
-    (uninitialised when allocated here)."""
+    (uninitialised when allocated here).  Autograd does not see the call: no
+    output has a grad_fn, and a training step calls moe_combine_rows without
+    weights for the gradient of bf16 rows with respect to x."""
     if quant not in _ROW_TYPE:
         raise AssertionError(f"quant: {quant!r}, expected None, 'fp8' or 'int8'")
     return _call("sort_rows", x, topk_ids, E, x_scale, _ROW_TYPE[quant], rows, scales, offsets, inv, scratch)
@@ -578,7 +580,9 @@ def moe_combine_rows(rows: torch.Tensor, inv: torch.Tensor, weights=None, out=No
     """The experts' bf16 rows [num_rows, cols] back at their tokens: out[t] =
     sum_j weights[t, j] rows[inv[t, j]] with inv from moe_sort_rows and fp32
     weights [T, topk] (None: 1, which makes it the gradient of moe_sort_rows with
-    respect to a bf16 x).  Returns bf16 out [T, cols]."""
+    respect to a bf16 x).  Returns bf16 out [T, cols], without a grad_fn also
+    where rows or weights require a gradient: that is moe_combine_rows_bwd's to
+    call for."""
     return _call("combine_rows", rows, inv, weights, out)
 
 
@@ -589,6 +593,8 @@ def moe_combine_rows_bwd(grad_out: torch.Tensor, inv: torch.Tensor, rows=None, w
     fp32 grad_weights[t, j] = grad_out[t] . rows[inv[t, j]].  grad_rows has as
     many rows as ``rows`` (without them T * topk when allocated here); rows that
     no slot has keep what they held (uninitialised when allocated here), and no
-    row may be named by two slots (moe_sort_rows names none twice).
+    row may be named by two slots (moe_sort_rows names none twice).  Nothing calls
+    this but its user: autograd records none of these operators, and the products
+    in between have no gradient here.
     Returns (grad_rows, grad_weights or None)."""
     return _call("combine_rows_bwd", grad_out, inv, rows, weights, grad_rows, grad_weights)

@@ -197,3 +197,21 @@ def test_combine_of_more_columns_than_a_launch_takes(weighted):
         if weighted:
             want *= w[part]
         assert torch.equal(out[part], want.bfloat16()), lo
+
+
+# ----------------------------------------------------------- autograd ---
+
+def test_no_output_has_a_grad_fn():
+    """Operands that require a gradient are taken, and nothing is recorded: the
+    gradients are calls of their own, as the docstrings say."""
+    d = dev()
+    x = torch.randn(9, 64, device=d).bfloat16().requires_grad_()
+    ids = torch.randint(0, 4, (9, 2), device=d, dtype=torch.int32)
+    w = torch.rand(9, 2, device=d, requires_grad=True)
+    rows, _, _, inv = ops.moe_sort_rows(x, ids, 4)
+    out = ops.moe_combine_rows(rows.requires_grad_(), inv, w)
+    grads = ops.moe_combine_rows_bwd(out, inv, rows=rows, weights=w)
+    for t in (out, *grads):
+        assert t.grad_fn is None and not t.requires_grad
+    for f in (ops.moe_sort_rows, ops.moe_combine_rows, ops.moe_combine_rows_bwd):
+        assert "autograd" in f.__doc__.lower() or "grad_fn" in f.__doc__
