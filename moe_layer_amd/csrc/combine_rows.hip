@@ -6,8 +6,9 @@
 // its weight's gradient is 0.
 //
 // Every row is read once and every output written once, so both are bound by bytes:
-// the combine of 8192 x 7168 and 8 slots 179-193 us, 5.5-5.9 TB/s (a large copy 5.1); the
-// gradient of 4096 x 4096 and 8 slots 113 us, 5.05 TB/s.  A thread has one piece of 16
+// the combine of 8192 x 7168 and 8 slots 193 us, 5.5 TB/s (a large copy 5.1), 179 where the
+// last output is in the last-level cache yet; the gradient of 4096 x 4096 and 8 slots 113
+// us, 5.05 TB/s.  A thread has one piece of 16
 // bytes of a token, which fills the CUs from a few tokens on, with the loads of eight
 // slots in flight; gathering by token needs no atomics and sums in slot order.
 #include "sorted.h"

@@ -46,10 +46,13 @@ constexpr Tile kTilesBf16[] = {
 };
 // int8: from the bf16 constants (as many bytes that go to the matrix cores as they
 // are) by a search for the ones whose picks are the fastest over 347 shapes, dense
-// and grouped, each timed in every tile: 2.3 % slower than the best tile in the
-// geometric mean, 45 % at worst (1568 rows in 100 groups of 360 x 128, 6.5 us); fitted
-// to half of them 2.8 % over the other half.  Without the two workgroups a CU of the last one
-// the best tile were 48 % slower at worst (7189 rows in 256 groups of 504 x 256).
+// and grouped, each timed in every tile; fitted to half of them 2.8 % above the best tile
+// over the other half.  The kernels have changed since then (few rows' K out of step,
+// stores): timed again, the picks are 2.3 % above the best tile in the geometric mean (155
+// dense shapes 1.4 %, 192 grouped 3.0 %), 44 % at worst (1568 rows in 100 groups of 360 x
+// 128, 6.6 us; dense 15 %, 1 x 104 x 512).  When fitted, the best tile without the two
+// workgroups a CU of the last one was 48 % slower at worst (7189 rows in 256 groups of
+// 504 x 256).
 constexpr Tile kTilesInt8[] = {
     {true, 0, 16, 16, 1.18f, 1.14f, 0.0561f},    {true, 1, 32, 16, 1.20f, 1.52f, 0.0748f},
     {true, 2, 32, 32, 1.03f, 1.24f, 0.1195f},    {true, 3, 64, 32, 0.79f, 2.11f, 0.1240f},

@@ -7,7 +7,7 @@
 // read once; the maximum of the row's bf16 bits is joined through lane permutations
 // and, where several waves have a row, LDS.  Rows of up to 32 chunks share a wave (24265
 // x 80 gated 4.6 us, a wave to a row 11.6).  Many rows are bound by their bytes
-// (32771 x 1536 gated 46.6 us, 5.4 TB/s), few by the launch (3.6-4 us).
+// (32771 x 1536 gated 46-47 us, 5.4 TB/s), few by the launch (3.6-4 us).
 #include "moe.h"
 
 #include "dev_silu.h"

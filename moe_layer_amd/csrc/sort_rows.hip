@@ -13,9 +13,13 @@
 //               (sort_place_kernel), then the rows are moved: three launches, for
 //               more ids than every workgroup should read.
 // A row is read once and stored topk times: large batches are bound by those bytes
-// (8192 x 7168 bf16 to 8 of 128 experts 187 us, x from the last-level cache, 216 with x
-// from HBM, 4.9 TB/s; 10 of them to find the positions), single tokens by the launch (kernel 2.8 us), batches in between by the
-// look at all ids in front (1031 x 4096 to int8 11.3 us, 8.3 of them bytes).
+// (8192 x 7168 bf16 to 8 of 256 experts 216 us with x from HBM, 4.9 TB/s, 187 with x from
+// the last-level cache; 10 of them to find the positions), single tokens by the launch
+// (kernel 2.7 us), batches in between by the look at all ids in front (1031 x 4096 to
+// int8 11.4 us, 8.3 of them bytes).  8 of 256 experts, in a graph, us (bytes at 5.07 TB/s):
+// to fp8 64 x 4096 4.5 (0.5), 1031 x 4096 12.3 (8.6), 8192 x 7168 105 (119); fp8 codes with
+// their scales 4.7 (0.5), 12.0 (7.7), 105 (108); int8 codes 1031 x 4096 12.2 (7.5), 8192 x
+// 7168 106 (104).
 #include "dev_align.h"
 #include "moe.h"
 #include "sorted.h"

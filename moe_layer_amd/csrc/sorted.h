@@ -97,8 +97,9 @@ hipError_t launch_quant_int8(const Int8Args& a, bool gated, hipStream_t s);
 // 6.5 TB/s and is written at up to 6, instead of 5.1, and evicts nothing; smaller ones
 // stay for the kernel that comes next.
 // Written so only where rows are whole lines, and read so where they are that or long:
-// lines that two rows share should meet in a cache (us as they are / past: 8192 tokens
-// of 8 slots, sort 7168 columns 208 / 184, 7176 246 / 249, 5000 166 / 176, 65536 of 1000
+// lines that two rows share should meet in a cache (us as they are / past, called on the
+// same rows again, so that x or the output is in the last-level cache: 8192 tokens of 8
+// slots, sort 7168 columns 208 / 184, 7176 246 / 249, 5000 166 / 176, 65536 of 1000
 // 277 / 295; combine 204 / 177, 203 / 185, 142 / 130, 226 / 215, 200000 of 328 226 / 234).
 constexpr int64_t kLastCacheBytes = int64_t(256) << 20;
 inline bool whole_lines(const void* rows, int64_t row_bytes) {
