@@ -9,6 +9,7 @@ import oracle as O
 from moe_layer_amd import ops
 
 from gpu_util import dev
+from test_gpu_sorted import KINDS, check_sort, routing
 
 pytestmark = pytest.mark.gpu
 
@@ -62,6 +63,30 @@ def test_sort_to_fp8_is_moe_quant_act_whatever_the_values(T, k, cols):
         at = inv[:, j].long()
         assert torch.equal(rows[at], codes)
         assert torch.equal(row_scales[at].view(torch.int32), scales.view(torch.int32))
+
+
+# --------------------------------- few tokens that count, many that compare ---
+
+@pytest.mark.parametrize("kind,quant", KINDS)
+@pytest.mark.parametrize("T,k,E,cols", [(32, 64, 100, 256), (33, 64, 1024, 256), (80, 64, 70, 640), (200, 33, 100, 1152),
+                                        (255, 64, 64, 128), (256, 16, 300, 512), (49, 64, 65, 17408)])
+def test_sort_of_few_tokens_with_many_slots(T, k, E, cols, kind, quant):
+    """Both sides of where up to 256 tokens' ids are counted, not compared."""
+    rng = np.random.default_rng(T + k)
+    check_sort(T, k, E, cols, kind, quant, routing(rng, T, k, E, away=0.1, repeats=k > E), T)
+
+
+def test_few_tokens_with_many_slots_past_the_last_cache():
+    d, T, k, E, cols = dev(), 256, 64, 128, 8192
+    g = torch.Generator(device=d).manual_seed(5)
+    x = torch.randn(T, cols, generator=g, device=d).bfloat16()
+    ids = torch.randint(-2, E + 2, (T, k), generator=g, device=d, dtype=torch.int32)
+    rows, _, offsets, inv = ops.moe_sort_rows(x, ids, E)
+    assert rows.nbytes >= 256 << 20
+    want_off, want_inv, token = O.sort_slots(ids.cpu().numpy(), E)
+    np.testing.assert_array_equal(offsets.cpu().numpy(), want_off)
+    np.testing.assert_array_equal(inv.cpu().numpy(), want_inv)
+    assert torch.equal(rows[:len(token)], x[torch.from_numpy(np.asarray(token)).long().to(d)])
 
 
 # ------------------------------------------------- the form with scratch ---
